@@ -12,6 +12,12 @@ because the kernels trust the sizes and strides they are given.
   decode(q, k, v, A_log, dt_bias, a, b, pool, read_idx, ...) -> (out, pool)
   conv1d(x, weight, conv_state, slot_idx, row_offsets, ...) -> out
   state_update(q, k, v, gamma, beta) -> {"outputs", "final_state"}
+
+and, for the softmax-attention layers beside them (paged.py):
+
+  attn_decode(q, k_cache, v_cache, page_table, lens, ...) -> out | (out, lse)
+  kv_append(k, v, k_cache, v_cache, page_table, lens, ...) -> (k_cache, v_cache)
+  pages_copy, pages_extend, pages_fork, pages_free, pages_compact
 """
 from __future__ import annotations
 
@@ -22,10 +28,14 @@ import torch
 
 from . import _lib
 from ._lib import GdnError
+from .paged import (attn_decode, attn_decode_args, attn_decode_workspace_size, kv_append, kv_append_args,
+                    pages_args, pages_compact, pages_copy, pages_extend, pages_fork, pages_free)
 
 __all__ = ["gate", "prefill", "decode", "conv1d", "state_update", "version", "GdnError",
            "prefill_args", "decode_args", "conv1d_args", "prefill_workspace_size",
-           "prefill_noalloc", "wait_timeouts"]
+           "prefill_noalloc", "wait_timeouts", "attn_decode", "attn_decode_args",
+           "attn_decode_workspace_size", "kv_append", "kv_append_args", "pages_copy", "pages_args",
+           "pages_extend", "pages_fork", "pages_free", "pages_compact"]
 
 _DT = {torch.float32: _lib.GDN_F32, torch.bfloat16: _lib.GDN_BF16}
 # update_rule of the ONNX card -> gdn_update_rule

@@ -294,4 +294,203 @@ gdn_status gdn_conv1d(const gdn_conv1d_args* p, void* stream) {
   return from_hip(gdn::launch_conv1d(a, (hipStream_t)stream), "gdn_conv1d launch");
 }
 
+// What the calls over a paged cache share: sizes, types and scales.
+static gdn_status cache_check(const char* f, int32_t batch, int32_t hkv, int32_t d, int32_t io_dtype,
+                              int32_t cache_dtype, int32_t n_pages, int32_t page_size, int32_t max_pages,
+                              int64_t table_stride, const float* k_scale, const float* v_scale) {
+  if (io_dtype != GDN_F32 && io_dtype != GDN_BF16) return fail(GDN_ERR_DTYPE, "%s: io_dtype %d", f, io_dtype);
+  if (cache_dtype != io_dtype && cache_dtype != GDN_E4M3)
+    return fail(GDN_ERR_DTYPE, "%s: cache_dtype %d (io_dtype's type or GDN_E4M3)", f, cache_dtype);
+  if (batch < 0 || hkv <= 0 || d <= 0 || n_pages < 0 || page_size <= 0 || max_pages < 0)
+    return fail(GDN_ERR_SHAPE, "%s: bad sizes batch=%d hkv=%d d=%d n_pages=%d page_size=%d max_pages=%d", f, batch,
+                hkv, d, n_pages, page_size, max_pages);
+  if (d != 32 && d != 64 && d != 128 && d != 256)
+    return fail(GDN_ERR_UNSUPPORTED, "%s: d=%d (supported: 32, 64, 128, 256)", f, d);
+  if ((int64_t)max_pages * page_size > (int64_t(1) << 30))
+    return fail(GDN_ERR_UNSUPPORTED, "%s: max_pages * page_size must be at most 2^30", f);
+  if (table_stride < max_pages) return fail(GDN_ERR_LAYOUT, "%s: page_table_stride smaller than max_pages", f);
+  if (cache_dtype == GDN_E4M3 && (!k_scale || !v_scale))
+    return fail(GDN_ERR_NULL, "%s: an e4m3 cache needs k_scale and v_scale", f);
+  if (cache_dtype != GDN_E4M3 && (k_scale || v_scale))
+    return fail(GDN_ERR_SHAPE, "%s: k_scale and v_scale are for e4m3 caches", f);
+  return GDN_OK;
+}
+
+// Strides of a [page, token, head, d] cache (es bytes an element): either
+// order of tokens and heads inside a page, nothing smaller than dense.
+static gdn_status cache_layout(const char* f, const void* base, int64_t page, int64_t token, int64_t head,
+                               int32_t page_size, int32_t hkv, int32_t d, size_t es) {
+  const int64_t unit = 16 / (int64_t)es, lim = int64_t(1) << 23;
+  if (!aligned(base, 16) || page < 0 || page % unit != 0 || token % unit != 0 || head % unit != 0)
+    return fail(GDN_ERR_LAYOUT, "%s: caches and their strides must be 16-byte aligned", f);
+  if (token < d || head < d || token >= lim || head >= lim)
+    return fail(GDN_ERR_LAYOUT, "%s: cache token and head strides must be in [d, 2^23)", f);
+  // one of the two orders must keep every row apart
+  if (token < (int64_t)(hkv - 1) * head + d && head < (int64_t)(page_size - 1) * token + d)
+    return fail(GDN_ERR_LAYOUT, "%s: cache rows overlap", f);
+  if (page < (int64_t)(page_size - 1) * token + (int64_t)(hkv - 1) * head + d)
+    return fail(GDN_ERR_LAYOUT, "%s: cache page stride smaller than a page", f);
+  return GDN_OK;
+}
+
+size_t gdn_attn_decode_workspace_size(const gdn_attn_decode_args* args) {
+  return args ? gdn::attn_workspace_bytes(*args) : 0;
+}
+
+gdn_status gdn_attn_decode(const gdn_attn_decode_args* p, void* stream) {
+  static const char* f = "gdn_attn_decode";
+  g_err[0] = 0;
+  if (!p) return fail(GDN_ERR_NULL, "%s: args is NULL", f);
+  const gdn_attn_decode_args& a = *p;
+  gdn_status st = cache_check(f, a.batch, a.hkv, a.d, a.io_dtype, a.cache_dtype, a.n_pages, a.page_size, a.max_pages,
+                              a.page_table_stride, a.k_scale, a.v_scale);
+  if (st != GDN_OK) return st;
+  if (a.T <= 0 || a.hq <= 0) return fail(GDN_ERR_SHAPE, "%s: bad sizes T=%d hq=%d", f, a.T, a.hq);
+  if (a.T > 64) return fail(GDN_ERR_UNSUPPORTED, "%s: T=%d (supported 1..64)", f, a.T);
+  if (a.hq % a.hkv != 0) return fail(GDN_ERR_SHAPE, "%s: hq=%d is not a multiple of hkv=%d", f, a.hq, a.hkv);
+  if (a.hq > 65536) return fail(GDN_ERR_UNSUPPORTED, "%s: hq=%d (supported up to 65536)", f, a.hq);
+  if (a.batch == 0) return GDN_OK;
+  // Each size is below 2^31 and hq at most 2^16: in this order no product overflows 64 bits.
+  if ((int64_t)a.batch * a.hq >= (int64_t(1) << 31) || (int64_t)a.batch * a.hq * a.T >= (int64_t(1) << 31))
+    return fail(GDN_ERR_UNSUPPORTED, "%s: batch * hq * T must be below 2^31", f);
+  // one workgroup per row, key-value head and 16 query rows; a grid has at most 2^24 of 256 threads
+  if ((int64_t)a.batch * a.hkv * (((int64_t)a.T * (a.hq / a.hkv) + 15) / 16) > (int64_t(1) << 23))
+    return fail(GDN_ERR_UNSUPPORTED, "%s: batch * hkv * ceil(T * hq / hkv / 16) must be at most 2^23", f);
+  if (!a.q || !a.out || !a.lens || (a.max_pages > 0 && !a.page_table) || (a.n_pages > 0 && (!a.k_cache || !a.v_cache)))
+    return fail(GDN_ERR_NULL, "%s: q, caches, page_table, lens and out are required", f);
+  const size_t es = elem_size(a.io_dtype), ce = a.cache_dtype == GDN_E4M3 ? 1 : es;
+  if (!aligned(a.q, 16) || !aligned(a.out, 16)) return fail(GDN_ERR_LAYOUT, "%s: q and out must be 16-byte aligned", f);
+  const int64_t unit = 16 / (int64_t)es;
+  if (a.q_stride_row < 0 || a.q_stride_token < 0 || a.q_stride_head < 0 || a.q_stride_row % unit != 0 ||
+      a.q_stride_token % unit != 0 || a.q_stride_head % unit != 0)
+    return fail(GDN_ERR_LAYOUT, "%s: q strides must be non-negative multiples of 16 bytes", f);
+  if (a.n_pages > 0) {
+    st = cache_layout(f, a.k_cache, a.k_stride_page, a.k_stride_token, a.k_stride_head, a.page_size, a.hkv, a.d, ce);
+    if (st != GDN_OK) return st;
+    st = cache_layout(f, a.v_cache, a.v_stride_page, a.v_stride_token, a.v_stride_head, a.page_size, a.hkv, a.d, ce);
+    if (st != GDN_OK) return st;
+  }
+  if (a.workspace && !aligned(a.workspace, 256)) return fail(GDN_ERR_LAYOUT, "%s: workspace must be 256-byte aligned", f);
+  return from_hip(gdn::launch_attn_decode(a, (hipStream_t)stream), "gdn_attn_decode launch");
+}
+
+gdn_status gdn_kv_append(const gdn_kv_append_args* p, void* stream) {
+  static const char* f = "gdn_kv_append";
+  g_err[0] = 0;
+  if (!p) return fail(GDN_ERR_NULL, "%s: args is NULL", f);
+  const gdn_kv_append_args& a = *p;
+  gdn_status st = cache_check(f, a.batch, a.hkv, a.d, a.io_dtype, a.cache_dtype, a.n_pages, a.page_size, a.max_pages,
+                              a.page_table_stride, a.k_scale, a.v_scale);
+  if (st != GDN_OK) return st;
+  if (a.total_tokens < 0) return fail(GDN_ERR_SHAPE, "%s: total_tokens=%lld", f, (long long)a.total_tokens);
+  if (a.hkv > 65536) return fail(GDN_ERR_UNSUPPORTED, "%s: hkv=%d (supported up to 65536)", f, a.hkv);
+  if (a.total_tokens > (int64_t(1) << 28)) return fail(GDN_ERR_UNSUPPORTED, "%s: total_tokens must be at most 2^28", f);
+  if (a.batch == 0 || a.total_tokens == 0) return GDN_OK;
+  if (!a.cu_seqlens && a.total_tokens % a.batch != 0)
+    return fail(GDN_ERR_SHAPE, "%s: without cu_seqlens total_tokens %lld must be a multiple of batch %d", f,
+                (long long)a.total_tokens, a.batch);
+  if (a.n_pages == 0 || a.max_pages == 0) return GDN_OK;  // no page to write to
+  if (!a.k || !a.v || !a.k_cache || !a.v_cache || !a.page_table || !a.lens)
+    return fail(GDN_ERR_NULL, "%s: k, v, caches, page_table and lens are required", f);
+  const size_t es = elem_size(a.io_dtype), ce = a.cache_dtype == GDN_E4M3 ? 1 : es;
+  const int64_t unit = 16 / (int64_t)es;
+  const int64_t strides[] = {a.k_stride_token, a.k_stride_head, a.v_stride_token, a.v_stride_head};
+  if (!aligned(a.k, 16) || !aligned(a.v, 16)) return fail(GDN_ERR_LAYOUT, "%s: k and v must be 16-byte aligned", f);
+  for (int64_t s : strides)
+    if (s < 0 || s % unit != 0) return fail(GDN_ERR_LAYOUT, "%s: k and v strides must be non-negative multiples of 16 bytes", f);
+  st = cache_layout(f, a.k_cache, a.kc_stride_page, a.kc_stride_token, a.kc_stride_head, a.page_size, a.hkv, a.d, ce);
+  if (st != GDN_OK) return st;
+  st = cache_layout(f, a.v_cache, a.vc_stride_page, a.vc_stride_token, a.vc_stride_head, a.page_size, a.hkv, a.d, ce);
+  if (st != GDN_OK) return st;
+  return from_hip(gdn::launch_kv_append(a, (hipStream_t)stream), "gdn_kv_append launch");
+}
+
+gdn_status gdn_pages_copy(void* pool, int64_t page_bytes, int64_t page_stride, int32_t n_pages, const int32_t* src,
+                          const int32_t* dst, int64_t n, void* stream) {
+  static const char* f = "gdn_pages_copy";
+  g_err[0] = 0;
+  if (page_bytes < 0 || n_pages < 0 || n < 0)
+    return fail(GDN_ERR_SHAPE, "%s: page_bytes=%lld n_pages=%d n=%lld", f, (long long)page_bytes, n_pages, (long long)n);
+  if (page_stride < page_bytes) return fail(GDN_ERR_LAYOUT, "%s: page_stride smaller than page_bytes", f);
+  if (n >= (int64_t(1) << 31) || page_bytes >= (int64_t(1) << 40))
+    return fail(GDN_ERR_UNSUPPORTED, "%s: n must be below 2^31 and page_bytes below 2^40", f);
+  if (n == 0 || page_bytes == 0 || n_pages == 0) return GDN_OK;
+  if (!pool || !src || !dst) return fail(GDN_ERR_NULL, "%s: pool, src and dst are required", f);
+  return from_hip(gdn::launch_pages_copy(pool, page_bytes, page_stride, n_pages, src, dst, n, (hipStream_t)stream),
+                  "gdn_pages_copy launch");
+}
+
+size_t gdn_pages_workspace_size(int32_t rows, int32_t n_pages) {
+  return rows < 0 || n_pages <= 0 ? 0 : gdn::pages_workspace_bytes(rows, n_pages);
+}
+
+// The checks that the page-table calls share; lens: whether the call has row lengths.
+static gdn_status pages_check(const char* f, const gdn_pages_args* p, bool lens, bool workspace) {
+  g_err[0] = 0;
+  if (!p) return fail(GDN_ERR_NULL, "%s: args is NULL", f);
+  const gdn_pages_args& a = *p;
+  if (a.rows < 0 || a.max_pages <= 0 || a.n_pages <= 0 || a.page_size <= 0)
+    return fail(GDN_ERR_SHAPE, "%s: bad sizes rows=%d max_pages=%d n_pages=%d page_size=%d", f, a.rows, a.max_pages,
+                a.n_pages, a.page_size);
+  if (a.n_pages > (1 << 24)) return fail(GDN_ERR_UNSUPPORTED, "%s: n_pages=%d (supported up to 2^24)", f, a.n_pages);
+  if (a.rows > (1 << 20)) return fail(GDN_ERR_UNSUPPORTED, "%s: rows=%d (supported up to 2^20)", f, a.rows);
+  if ((int64_t)a.max_pages * a.page_size > (int64_t(1) << 30))
+    return fail(GDN_ERR_UNSUPPORTED, "%s: max_pages * page_size must be at most 2^30", f);
+  if (a.page_table_stride < a.max_pages || a.page_table_out_stride < a.max_pages)
+    return fail(GDN_ERR_LAYOUT, "%s: row strides smaller than max_pages", f);
+  if (!a.refs || !a.refs_out || (a.rows > 0 && (!a.page_table || !a.page_table_out)) ||
+      (lens && a.rows > 0 && (!a.lens || !a.lens_out)))
+    return fail(GDN_ERR_NULL, "%s: page_table, refs%s and their outputs are required", f, lens ? ", lens" : "");
+  if (a.page_table == a.page_table_out && a.rows > 1 && a.page_table_stride != a.page_table_out_stride)
+    return fail(GDN_ERR_LAYOUT, "%s: page_table in place needs equal strides", f);
+  if (workspace) {
+    if (!a.workspace) return fail(GDN_ERR_NULL, "%s: workspace is required", f);
+    if (!aligned(a.workspace, 256)) return fail(GDN_ERR_LAYOUT, "%s: workspace must be 256-byte aligned", f);
+    if (a.workspace_bytes < gdn::pages_workspace_bytes(a.rows, a.n_pages))
+      return fail(GDN_ERR_SHAPE, "%s: workspace of %zu bytes (%zu needed)", f, a.workspace_bytes,
+                  gdn::pages_workspace_bytes(a.rows, a.n_pages));
+  }
+  return GDN_OK;
+}
+
+gdn_status gdn_pages_extend(const gdn_pages_args* p, const int32_t* add, int32_t* ok, void* stream) {
+  const gdn_status st = pages_check("gdn_pages_extend", p, true, true);
+  if (st != GDN_OK) return st;
+  if (p->rows > 0 && (!add || !ok)) return fail(GDN_ERR_NULL, "gdn_pages_extend: add and ok are required");
+  return from_hip(gdn::launch_pages_extend(*p, add, ok, (hipStream_t)stream), "gdn_pages_extend launch");
+}
+
+gdn_status gdn_pages_fork(const gdn_pages_args* p, const int32_t* parent, int32_t* src, int32_t* dst, void* stream) {
+  const gdn_status st = pages_check("gdn_pages_fork", p, true, true);
+  if (st != GDN_OK) return st;
+  if (p->rows > 0) {
+    if (!parent || !src || !dst) return fail(GDN_ERR_NULL, "gdn_pages_fork: parent, src and dst are required");
+    const char* i0 = (const char*)p->page_table;
+    const char* o0 = (const char*)p->page_table_out;
+    const size_t in = ((size_t)(p->rows - 1) * p->page_table_stride + p->max_pages) * 4;
+    const size_t out = ((size_t)(p->rows - 1) * p->page_table_out_stride + p->max_pages) * 4;
+    const char* l0 = (const char*)p->lens;
+    const char* m0 = (const char*)p->lens_out;
+    const size_t ln = (size_t)p->rows * 4;
+    if ((i0 < o0 + out && o0 < i0 + in) || (l0 < m0 + ln && m0 < l0 + ln))
+      return fail(GDN_ERR_LAYOUT, "gdn_pages_fork: page_table_out and lens_out must be apart from the inputs");
+  }
+  return from_hip(gdn::launch_pages_fork(*p, parent, src, dst, (hipStream_t)stream), "gdn_pages_fork launch");
+}
+
+gdn_status gdn_pages_free(const gdn_pages_args* p, const uint8_t* mask, void* stream) {
+  const gdn_status st = pages_check("gdn_pages_free", p, true, false);
+  if (st != GDN_OK) return st;
+  if (p->rows > 0 && !mask) return fail(GDN_ERR_NULL, "gdn_pages_free: mask is required");
+  return from_hip(gdn::launch_pages_free(*p, mask, (hipStream_t)stream), "gdn_pages_free launch");
+}
+
+gdn_status gdn_pages_compact(const gdn_pages_args* p, int32_t* src, int32_t* dst, int32_t* n_live, void* stream) {
+  const gdn_status st = pages_check("gdn_pages_compact", p, false, true);
+  if (st != GDN_OK) return st;
+  if (!n_live || (p->n_pages > 1 && (!src || !dst)))
+    return fail(GDN_ERR_NULL, "gdn_pages_compact: src, dst and n_live are required");
+  return from_hip(gdn::launch_pages_compact(*p, src, dst, n_live, (hipStream_t)stream), "gdn_pages_compact launch");
+}
+
 }  // extern "C"

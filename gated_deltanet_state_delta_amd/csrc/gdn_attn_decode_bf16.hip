@@ -1,0 +1,8 @@
+// gdn_attn_decode_bf16.hip -- attention over a paged cache, one instantiation set.
+#include "gdn_attn_decode.hpp"
+
+namespace gdn {
+hipError_t launch_attn_bf16(const AttnParams& p, int d, dim3 grid, hipStream_t stream) {
+  return launch_attn_t<__bf16, __bf16>(p, d, grid, stream);
+}
+}  // namespace gdn

@@ -1,0 +1,8 @@
+// gdn_attn_decode_f32_e4m3.hip -- attention over a paged cache, one instantiation set.
+#include "gdn_attn_decode.hpp"
+
+namespace gdn {
+hipError_t launch_attn_f32_e4m3(const AttnParams& p, int d, dim3 grid, hipStream_t stream) {
+  return launch_attn_t<float, e4m3>(p, d, grid, stream);
+}
+}  // namespace gdn

@@ -1,0 +1,484 @@
+// gdn_pages.hip -- the pages of a cache: contents copied between pages, and
+// page tables grown, forked, freed and compacted on the device.
+//
+// A page is free when refs[page] == 0.  Pages are always taken lowest first,
+// in row order, so every result is determined by the inputs; counts are
+// changed with integer atomics only, whose order does not matter.  Nothing is
+// read on the host: sizes fix the launches, and the lists that a call emits
+// are padded with -1.
+//
+// The calls are launch-bound at serving sizes (a few MB of tables and
+// counts).  Ranking free pages takes two passes over the counts, tile by
+// tile: every workgroup counts its tile, then every workgroup sums the counts
+// of the tiles before its own and ranks inside it -- no workgroup waits for
+// another inside a launch.
+#include "gdn_device.hpp"
+#include "gdn_kernels.hpp"
+
+namespace gdn {
+
+// ------------------------------------------------------------------- copy --
+
+// 16 bytes at any alignment.
+typedef u32x4 u32x4_any __attribute__((aligned(1)));
+
+constexpr int kCopyChunk = 32768;  // bytes of a page that one workgroup copies at a time
+
+// Pieces of 16 bytes, four loads in flight per thread; the last bytes of a
+// page one by one.  Workgroups step over (pair, chunk) items, so a list that
+// is mostly -1 costs its reading only.
+__global__ void __launch_bounds__(256) pages_copy_kernel(char* pool, int64_t page_bytes, int64_t stride, int n_pages,
+                                                         const int32_t* src, const int32_t* dst, int64_t items,
+                                                         uint32_t chunks) {
+  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const int64_t pair = it / chunks;
+    const int s = src[pair], d = dst[pair];
+    if (s < 0 || s >= n_pages || d < 0 || d >= n_pages || s == d) continue;
+    const int64_t at = (it - pair * chunks) * kCopyChunk;
+    const int bytes = (int)min((int64_t)kCopyChunk, page_bytes - at), vec = bytes / 16;
+    const char* from = pool + s * stride + at;
+    char* to = pool + d * stride + at;
+    int i = threadIdx.x;
+    for (; i + 768 < vec; i += 1024) {
+      u32x4 t[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) t[k] = *reinterpret_cast<const u32x4_any*>(from + (int64_t)(i + 256 * k) * 16);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) *reinterpret_cast<u32x4_any*>(to + (int64_t)(i + 256 * k) * 16) = t[k];
+    }
+    for (; i < vec; i += 256)
+      *reinterpret_cast<u32x4_any*>(to + (int64_t)i * 16) = *reinterpret_cast<const u32x4_any*>(from + (int64_t)i * 16);
+    if ((int)threadIdx.x < bytes - vec * 16) to[vec * 16 + threadIdx.x] = from[vec * 16 + threadIdx.x];
+  }
+}
+
+hipError_t launch_pages_copy(void* pool, int64_t page_bytes, int64_t stride, int n_pages, const int32_t* src,
+                             const int32_t* dst, int64_t n, hipStream_t stream) {
+  const int64_t chunks = (page_bytes + kCopyChunk - 1) / kCopyChunk, items = n * chunks;
+  const dim3 grid((unsigned)(items < 16384 ? items : 16384));
+  hipLaunchKernelGGL(pages_copy_kernel, grid, dim3(256), 0, stream, (char*)pool, page_bytes, stride, n_pages, src, dst,
+                     items, (uint32_t)chunks);
+  return hipGetLastError();
+}
+
+// ----------------------------------------------------------- tile ranking --
+
+constexpr int kTile = 1024;  // pages of one workgroup, 4 a thread
+
+struct PagesParams {
+  const int32_t* table;
+  const int32_t* lens;
+  const int32_t* refs;
+  int32_t* table_out;
+  int32_t* lens_out;
+  int32_t* refs_out;
+  int64_t table_stride, table_out_stride;
+  int rows, max_pages, n_pages, page_size, tiles;
+  // workspace: counts of a tile, ranked pages, per row and per page scratch
+  int32_t* tile_n;
+  int32_t* list;
+  int32_t* row_a;
+  int32_t* row_b;
+  int32_t* row_c;
+  int32_t* page_a;
+  int32_t* page_b;
+  int32_t* page_c;
+  int32_t* total;
+};
+
+// Sum over the workgroup's 256 threads, in every thread.
+__device__ __forceinline__ int block_sum(int v, int* lds) {
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return lds[0] + lds[1] + lds[2] + lds[3];
+}
+// Sum of the values of the threads before this one; `all` gets the whole sum.
+__device__ __forceinline__ int block_before(int v, int* lds, int& all) {
+  int s = v;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  for (int o = 1; o < 64; o <<= 1) {
+    const int t = __shfl_up(s, o);
+    if (lane >= o) s += t;
+  }
+  __syncthreads();
+  if (lane == 63) lds[w] = s;
+  __syncthreads();
+  int base = 0;
+  for (int i = 0; i < w; ++i) base += lds[i];
+  all = lds[0] + lds[1] + lds[2] + lds[3];
+  return base + s - v;
+}
+
+__device__ __forceinline__ int row_len(const PagesParams& p, const int32_t* lens, int r) {
+  const int cap = p.max_pages * p.page_size;
+  return min(max(lens[r], 0), cap);
+}
+__device__ __forceinline__ int pages_of(const PagesParams& p, int len) { return (int)(((int64_t)len + p.page_size - 1) / p.page_size); }
+__device__ __forceinline__ bool is_page(const PagesParams& p, int e) { return e >= 0 && e < p.n_pages; }
+
+// refs -> refs_out, and how many pages of each tile are free.
+// LIVE counts pages in use instead.
+template <bool LIVE>
+__device__ __forceinline__ void count_tile(const PagesParams& p, const int32_t* refs, bool copy, int* lds) {
+  int n = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int64_t i = (int64_t)blockIdx.x * kTile + k * 256 + threadIdx.x;
+    if (i < p.n_pages) {
+      const int v = refs[i];
+      n += LIVE ? v > 0 : v == 0;
+      if (copy) p.refs_out[i] = v;
+    }
+  }
+  n = block_sum(n, lds);
+  if (threadIdx.x == 0) p.tile_n[blockIdx.x] = n;
+}
+// Sums of tile_n before this tile, and of all.
+__device__ __forceinline__ int tiles_before(const PagesParams& p, int tile, int* lds, int& all) {
+  int a = 0, t = 0;
+  for (int i = threadIdx.x; i < p.tiles; i += 256) {
+    const int v = p.tile_n[i];
+    t += v;
+    if (i < tile) a += v;
+  }
+  all = block_sum(t, lds);
+  return block_sum(a, lds);
+}
+// The tile's free pages to their ranks in `list`.
+__device__ __forceinline__ void rank_tile(const PagesParams& p, const int32_t* refs, int* lds) {
+  int all;
+  int base = tiles_before(p, blockIdx.x, lds, all);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.total = all;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int64_t i = (int64_t)blockIdx.x * kTile + k * 256 + threadIdx.x;
+    const bool f = i < p.n_pages && refs[i] == 0;
+    int n;
+    const int at = block_before(f, lds, n);
+    if (f) p.list[base + at] = (int)i;
+    base += n;
+  }
+}
+
+// ----------------------------------------------------------------- extend --
+
+__global__ void __launch_bounds__(256) extend_count_kernel(PagesParams p) {
+  __shared__ int lds[4];
+  count_tile<false>(p, p.refs, p.refs_out != p.refs, lds);
+}
+
+// Tiles rank their free pages; the last workgroup walks the rows in order:
+// a row is served if the pages needed up to and with it are there.
+__global__ void __launch_bounds__(256) extend_rank_kernel(PagesParams p, const int32_t* add, int32_t* ok_out) {
+  __shared__ int lds[4];
+  if ((int)blockIdx.x < p.tiles) return rank_tile(p, p.refs, lds);
+  int n_free;
+  tiles_before(p, 0, lds, n_free);
+  int64_t before = 0;  // pages needed by the rows of earlier steps
+  for (int r0 = 0; r0 < p.rows; r0 += 256) {
+    const int r = r0 + threadIdx.x;
+    int len = 0, have = 0, need = 0;
+    int64_t grown = 0;
+    bool fits = false;
+    if (r < p.rows) {
+      len = row_len(p, p.lens, r);
+      grown = (int64_t)len + max(add[r], 0);
+      fits = grown <= (int64_t)p.max_pages * p.page_size;
+      have = pages_of(p, len);
+      if (fits) need = pages_of(p, (int)grown) - have;
+    }
+    int all;
+    const int at = block_before(need, lds, all);
+    if (r < p.rows) {
+      const int64_t upto = before + at + need;
+      const bool ok = fits && (need == 0 || upto <= n_free);
+      p.row_a[r] = ok ? (int)(upto - need) : 0;
+      p.row_b[r] = have;
+      p.row_c[r] = ok ? need : 0;
+      ok_out[r] = ok;
+      p.lens_out[r] = ok ? (int)grown : len;
+    }
+    before += all;
+  }
+}
+
+__global__ void __launch_bounds__(256) extend_assign_kernel(PagesParams p) {
+  const int r = blockIdx.x;
+  const int start = p.row_a[r], have = p.row_b[r], n = p.row_c[r];
+  const int32_t* from = p.table + r * p.table_stride;
+  int32_t* to = p.table_out + r * p.table_out_stride;
+  for (int i = threadIdx.x; i < p.max_pages; i += 256) {
+    int v = from[i];
+    if (i >= have && i < have + n) {
+      v = p.list[start + i - have];
+      p.refs_out[v] = 1;
+    }
+    to[i] = v;
+  }
+}
+
+// ------------------------------------------------------------------- fork --
+
+__global__ void __launch_bounds__(256) fork_init_kernel(PagesParams p) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= p.n_pages) return;
+  if (p.refs_out != p.refs) p.refs_out[i] = p.refs[i];
+  p.page_a[i] = 0x7fffffff;  // lowest row that holds the page as its part-filled last one
+  p.page_b[i] = 0;           // how many such rows
+}
+
+__global__ void __launch_bounds__(256) fork_rows_kernel(PagesParams p, const int32_t* parent) {
+  const int r = blockIdx.x, from = parent[r];
+  const bool has = from >= 0 && from < p.rows;
+  const int len = has ? row_len(p, p.lens, from) : 0, used = pages_of(p, len);
+  const int32_t* src = p.table + (has ? from : 0) * p.table_stride;
+  const int32_t* old = p.table + r * p.table_stride;
+  int32_t* to = p.table_out + r * p.table_out_stride;
+  const int was = pages_of(p, row_len(p, p.lens, r));
+  for (int i = threadIdx.x; i < p.max_pages; i += 256) {
+    const int v = i < used ? src[i] : -1;
+    to[i] = v;
+    if (from == r) continue;  // keeps what it holds
+    if (is_page(p, v)) atomicAdd(&p.refs_out[v], 1);
+    if (i < was && is_page(p, old[i])) atomicSub(&p.refs_out[old[i]], 1);
+  }
+  if (threadIdx.x == 0) {
+    p.lens_out[r] = len;
+    if (len % p.page_size != 0) {
+      const int last = src[len / p.page_size];
+      if (is_page(p, last)) {
+        atomicMin(&p.page_a[last], r);
+        atomicAdd(&p.page_b[last], 1);
+      }
+    }
+  }
+}
+
+// Tiles count their free pages; the last workgroup ranks the rows that need
+// a copy of their part-filled page.
+__global__ void __launch_bounds__(256) fork_count_kernel(PagesParams p) {
+  __shared__ int lds[4];
+  if ((int)blockIdx.x < p.tiles) return count_tile<false>(p, p.refs_out, false, lds);
+  int before = 0;
+  for (int r0 = 0; r0 < p.rows; r0 += 256) {
+    const int r = r0 + threadIdx.x;
+    bool copies = false;
+    if (r < p.rows) {
+      const int len = p.lens_out[r];
+      if (len % p.page_size != 0) {
+        const int last = p.table_out[r * p.table_out_stride + len / p.page_size];
+        copies = is_page(p, last) && !(p.page_a[last] == r && p.page_b[last] == p.refs_out[last]);
+      }
+    }
+    int all;
+    const int at = block_before(copies, lds, all);
+    if (r < p.rows) p.row_a[r] = copies ? before + at : -1;
+    before += all;
+  }
+}
+
+__global__ void __launch_bounds__(256) fork_rank_kernel(PagesParams p) {
+  __shared__ int lds[4];
+  rank_tile(p, p.refs_out, lds);
+}
+
+__global__ void __launch_bounds__(256) fork_assign_kernel(PagesParams p, int32_t* src, int32_t* dst) {
+  const int r = blockIdx.x, rank = p.row_a[r];
+  const bool served = rank >= 0 && rank < *p.total;
+  if (rank >= 0 && !served) {  // no page left: the row ends empty
+    int32_t* to = p.table_out + r * p.table_out_stride;
+    for (int i = threadIdx.x; i < p.max_pages; i += 256) {
+      if (is_page(p, to[i])) atomicSub(&p.refs_out[to[i]], 1);
+      to[i] = -1;
+    }
+    if (threadIdx.x == 0) p.lens_out[r] = 0;
+  }
+  if (threadIdx.x == 0) {
+    int s = -1, d = -1;
+    if (served) {
+      int32_t* e = p.table_out + r * p.table_out_stride + p.lens_out[r] / p.page_size;
+      s = *e;
+      d = p.list[rank];
+      *e = d;
+      atomicSub(&p.refs_out[s], 1);
+      p.refs_out[d] = 1;
+    }
+    src[r] = s;
+    dst[r] = d;
+  }
+}
+
+// ------------------------------------------------------------------- free --
+
+__global__ void __launch_bounds__(256) refs_copy_kernel(PagesParams p) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < p.n_pages) p.refs_out[i] = p.refs[i];
+}
+
+__global__ void __launch_bounds__(256) free_rows_kernel(PagesParams p, const uint8_t* mask) {
+  const int r = blockIdx.x;
+  const bool out = mask[r] != 0;
+  const int len = row_len(p, p.lens, r), used = pages_of(p, len);
+  const int32_t* from = p.table + r * p.table_stride;
+  int32_t* to = p.table_out + r * p.table_out_stride;
+  for (int i = threadIdx.x; i < p.max_pages; i += 256) {
+    const int v = from[i];
+    if (out && i < used && is_page(p, v)) atomicSub(&p.refs_out[v], 1);
+    to[i] = out ? -1 : v;
+  }
+  __syncthreads();  // every thread has read the row's length
+  if (threadIdx.x == 0) p.lens_out[r] = out ? 0 : len;
+}
+
+// ---------------------------------------------------------------- compact --
+
+__global__ void __launch_bounds__(256) compact_count_kernel(PagesParams p) {
+  __shared__ int lds[4];
+  count_tile<true>(p, p.refs, false, lds);
+}
+
+// With n_live pages in use: list[i] = the i-th free page below n_live;
+// page_a[p] = i for the i-th used page at or above it (-1: not used), with
+// page_b[i] = that page and page_c[i] = its count.
+__global__ void __launch_bounds__(256) compact_rank_kernel(PagesParams p) {
+  __shared__ int lds[4];
+  int n_live;
+  int base = tiles_before(p, blockIdx.x, lds, n_live);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.total = n_live;
+  // used pages below n_live: whole tiles, then the tile that n_live falls into
+  const int edge = n_live / kTile;
+  int unused_all;
+  int front = tiles_before(p, edge, lds, unused_all);
+  if (edge < p.tiles) {
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t i = (int64_t)edge * kTile + k * 256 + threadIdx.x;
+      if (i < n_live) n += p.refs[i] > 0;
+    }
+    front += block_sum(n, lds);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int64_t i = (int64_t)blockIdx.x * kTile + k * 256 + threadIdx.x;
+    const int v = i < p.n_pages ? p.refs[i] : 0;
+    int n;
+    const int rank = base + block_before(v > 0, lds, n);  // used pages before page i
+    if (i < p.n_pages) {
+      if (i < n_live) {
+        if (v <= 0) p.list[i - rank] = (int)i;
+      } else {
+        p.page_a[i] = v > 0 ? rank - front : -1;
+        if (v > 0) {
+          p.page_b[rank - front] = (int)i;
+          p.page_c[rank - front] = v;
+        }
+      }
+    }
+    base += n;
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.total[1] = n_live - front;  // pages that move
+}
+
+// The first rows workgroups rewrite the table, the others counts and moves.
+__global__ void __launch_bounds__(256) compact_apply_kernel(PagesParams p, int32_t* src, int32_t* dst, int32_t* n_live_out) {
+  const int n_live = p.total[0], moves = p.total[1];
+  if ((int)blockIdx.x < p.rows) {
+    const int r = blockIdx.x;
+    const int32_t* from = p.table + r * p.table_stride;
+    int32_t* to = p.table_out + r * p.table_out_stride;
+    for (int i = threadIdx.x; i < p.max_pages; i += 256) {
+      int v = from[i];
+      if (v >= n_live && v < p.n_pages) {
+        const int at = p.page_a[v];
+        if (at >= 0) v = p.list[at];
+      }
+      to[i] = v;
+    }
+    return;
+  }
+  const int64_t i = (int64_t)(blockIdx.x - p.rows) * 256 + threadIdx.x;
+  if (i >= p.n_pages) return;
+  if (i >= n_live) p.refs_out[i] = 0;
+  else if (p.refs_out != p.refs && p.refs[i] > 0) p.refs_out[i] = p.refs[i];
+  if (i < moves) p.refs_out[p.list[i]] = p.page_c[i];
+  if (i < p.n_pages / 2) {
+    src[i] = i < moves ? p.page_b[i] : -1;
+    dst[i] = i < moves ? p.list[i] : -1;
+  }
+  if (i == 0) *n_live_out = n_live;
+}
+
+// ----------------------------------------------------------------- launch --
+
+// Workspace, in int32 words: [total, padded to 64][tile counts][list, page_a,
+// page_b, page_c: n_pages each][row_a, row_b, row_c: rows each].
+size_t pages_workspace_bytes(int64_t rows, int64_t n_pages) {
+  const int64_t tiles = (n_pages + kTile - 1) / kTile;
+  return (size_t)(64 + tiles + 4 * n_pages + 3 * rows) * sizeof(int32_t);
+}
+
+static PagesParams pages_params(const gdn_pages_args& a) {
+  PagesParams p;
+  p.table = a.page_table;
+  p.lens = a.lens;
+  p.refs = a.refs;
+  p.table_out = a.page_table_out;
+  p.lens_out = a.lens_out;
+  p.refs_out = a.refs_out;
+  p.table_stride = a.page_table_stride;
+  p.table_out_stride = a.page_table_out_stride;
+  p.rows = a.rows;
+  p.max_pages = a.max_pages;
+  p.n_pages = a.n_pages;
+  p.page_size = a.page_size;
+  p.tiles = (a.n_pages + kTile - 1) / kTile;
+  p.total = (int32_t*)a.workspace;
+  p.tile_n = p.total + 64;
+  p.list = p.tile_n + p.tiles;
+  p.page_a = p.list + a.n_pages;
+  p.page_b = p.page_a + a.n_pages;
+  p.page_c = p.page_b + a.n_pages;
+  p.row_a = p.page_c + a.n_pages;
+  p.row_b = p.row_a + a.rows;
+  p.row_c = p.row_b + a.rows;
+  return p;
+}
+
+hipError_t launch_pages_extend(const gdn_pages_args& a, const int32_t* add, int32_t* ok, hipStream_t stream) {
+  const PagesParams p = pages_params(a);
+  hipLaunchKernelGGL(extend_count_kernel, dim3(p.tiles), dim3(256), 0, stream, p);
+  hipLaunchKernelGGL(extend_rank_kernel, dim3(p.tiles + 1), dim3(256), 0, stream, p, add, ok);
+  if (p.rows > 0) hipLaunchKernelGGL(extend_assign_kernel, dim3(p.rows), dim3(256), 0, stream, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_pages_fork(const gdn_pages_args& a, const int32_t* parent, int32_t* src, int32_t* dst, hipStream_t stream) {
+  const PagesParams p = pages_params(a);
+  hipLaunchKernelGGL(fork_init_kernel, dim3((p.n_pages + 255) / 256), dim3(256), 0, stream, p);
+  if (p.rows > 0) hipLaunchKernelGGL(fork_rows_kernel, dim3(p.rows), dim3(256), 0, stream, p, parent);
+  hipLaunchKernelGGL(fork_count_kernel, dim3(p.tiles + 1), dim3(256), 0, stream, p);
+  hipLaunchKernelGGL(fork_rank_kernel, dim3(p.tiles), dim3(256), 0, stream, p);
+  if (p.rows > 0) hipLaunchKernelGGL(fork_assign_kernel, dim3(p.rows), dim3(256), 0, stream, p, src, dst);
+  return hipGetLastError();
+}
+
+hipError_t launch_pages_free(const gdn_pages_args& a, const uint8_t* mask, hipStream_t stream) {
+  const PagesParams p = pages_params(a);
+  if (p.refs_out != p.refs)
+    hipLaunchKernelGGL(refs_copy_kernel, dim3((p.n_pages + 255) / 256), dim3(256), 0, stream, p);
+  if (p.rows > 0) hipLaunchKernelGGL(free_rows_kernel, dim3(p.rows), dim3(256), 0, stream, p, mask);
+  return hipGetLastError();
+}
+
+hipError_t launch_pages_compact(const gdn_pages_args& a, int32_t* src, int32_t* dst, int32_t* n_live, hipStream_t stream) {
+  const PagesParams p = pages_params(a);
+  hipLaunchKernelGGL(compact_count_kernel, dim3(p.tiles), dim3(256), 0, stream, p);
+  hipLaunchKernelGGL(compact_rank_kernel, dim3(p.tiles), dim3(256), 0, stream, p);
+  hipLaunchKernelGGL(compact_apply_kernel, dim3(p.rows + (p.n_pages + 255) / 256), dim3(256), 0, stream, p, src, dst, n_live);
+  return hipGetLastError();
+}
+
+}  // namespace gdn

@@ -49,7 +49,8 @@ typedef enum {
   GDN_ERR_HIP = 6          /* a HIP launch failed; gdn_last_error() has the text   */
 } gdn_status;
 
-typedef enum { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype;
+/* GDN_E4M3 (OCP 8-bit float, largest value 448) is a type of key-value caches only. */
+typedef enum { GDN_F32 = 0, GDN_BF16 = 1, GDN_E4M3 = 2 } gdn_dtype;
 
 /* update_rule of "com.microsoft.GatedDeltaNet" (Attributes): which terms of
  *   S_t = exp(g_t) S_{t-1} + k_t (beta_t (v_t - exp(g_t) S_{t-1}^T k_t))^T
@@ -407,6 +408,200 @@ typedef struct {
 } gdn_conv1d_args;
 
 gdn_status gdn_conv1d(const gdn_conv1d_args* args, void* stream);
+
+/* ============================================================================
+ * Paged key-value caches: the softmax-attention layers of a model that also
+ * has gated-delta-rule layers, served beside gdn_decode's state pool.
+ *
+ * A cache is an array of n_pages pages of page_size tokens, each token hkv
+ * heads of d elements: element (page, slot, head, i) lies at
+ *     cache + page*stride_page + slot*stride_token + head*stride_head + i
+ * (elements; tokens before heads or heads before tokens).  A batch row's
+ * tokens are found through its page table row: position j is slot
+ * j % page_size of page page_table[b][j / page_size], and lens[b] (clamped to
+ * [0, max_pages*page_size]) is how many positions it holds.  Table entries
+ * outside [0, n_pages) hold nothing: they are never read through or written
+ * through.  One table serves every layer whose caches have its page count.
+ *
+ *   page_table  [batch, max_pages] int32, rows page_table_stride apart
+ *   lens        [batch] int32
+ *   k_scale, v_scale  [hkv] fp32: the factor of each head's stored values,
+ *               given for GDN_E4M3 caches and NULL for the others
+ * Common requirements: max_pages * page_size at most 2^30; d in {32, 64, 128,
+ * 256}; hq a multiple of hkv (query head h reads key-value head h*hkv/hq);
+ * a cache has io_dtype's type or GDN_E4M3; caches, q, k, v and out 16-byte
+ * aligned, their strides multiples of 16 bytes, not smaller than the dense
+ * extents of what they step over (a cache's token and head strides each at
+ * least d) and, for token and head strides, below 2^23 elements.
+ * ========================================================================= */
+
+/* ----------------------------------------------------------------------------
+ * gdn_attn_decode -- attention of each row's newest T tokens over the cache.
+ *
+ * The cache already holds the new tokens (gdn_kv_append): token t of row b is
+ * position lens[b] - T + t, and sees the positions up to and with its own:
+ *     s_j = scale * k_scale[g] * <q[b,t,h], K[b,j,g]>,   g = h*hkv/hq
+ *     out[b,t,h] = v_scale[g] * sum_j e^{s_j} V[b,j,g] / sum_j e^{s_j}
+ *     lse[b,t,h] = log sum_j e^{s_j}
+ * A token that sees nothing (a row of no tokens, a position below 0, only
+ * invalid pages) gets zeros and lse -inf.  Values at positions that a token
+ * does not see never reach its result, infinities and NaN included.  Sums and
+ * the softmax are fp32; bf16 weights enter the product as two bf16 terms.
+ *
+ *   q    [batch, T, hq, d] io_dtype, strides {row, token, head}
+ *   out  [batch, T, hq, d] io_dtype, dense
+ *   lse  [batch, T, hq] fp32 or NULL
+ * 1 <= T <= 64, hq <= 65536; batch * hq * T below 2^31 and at most 2^23 groups
+ * (row, key-value head, 16 of its T*hq/hkv query rows), GDN_ERR_UNSUPPORTED
+ * above.  batch == 0 is a no-op.  Rows of the batch are independent:
+ * tables may share pages.
+ *
+ * With a workspace of at least gdn_attn_decode_workspace_size(args) bytes
+ * (device memory, 256-byte aligned; 0 when none is of use) the rows' lengths
+ * are split over workgroups and joined by a second launch; with less, one
+ * workgroup walks each row and key-value head: the same result up to rounding
+ * order.  The size depends on sizes alone, not on lens.  The library keeps
+ * nothing in the workspace between calls; calls that share one must not
+ * overlap.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t batch, T, hq, hkv, d;
+  int32_t io_dtype, cache_dtype;
+  float scale;              /* applied as given */
+  const void* q;
+  int64_t q_stride_row, q_stride_token, q_stride_head;
+  const void* k_cache;
+  int64_t k_stride_page, k_stride_token, k_stride_head;
+  const void* v_cache;
+  int64_t v_stride_page, v_stride_token, v_stride_head;
+  int32_t n_pages, page_size, max_pages;
+  const int32_t* page_table;
+  int64_t page_table_stride;
+  const int32_t* lens;
+  const float* k_scale;
+  const float* v_scale;
+  void* out;
+  float* lse;
+  void* workspace;
+  size_t workspace_bytes;
+} gdn_attn_decode_args;
+
+size_t gdn_attn_decode_workspace_size(const gdn_attn_decode_args* args);
+gdn_status gdn_attn_decode(const gdn_attn_decode_args* args, void* stream);
+
+/* ----------------------------------------------------------------------------
+ * gdn_kv_append -- new tokens' keys and values into their pages.
+ *
+ * lens already counts the new tokens: row b's n_b tokens go to positions
+ * lens[b] - n_b .. lens[b] - 1, in order.  Tokens whose position is negative
+ * or past the table, or whose page entry is invalid, are not written.  An
+ * e4m3 cache stores x / scale of the head, rounded to nearest even, clamped
+ * to +-448 (NaN stays NaN); others store x as it is.
+ *
+ *   k, v  [total_tokens, hkv, d] io_dtype, strides {token, head}
+ *   cu_seqlens  [batch + 1] int32: row b's tokens are cu_seqlens[b] ..
+ *         cu_seqlens[b+1] - 1 (clamped to [0, total_tokens], a decreasing pair
+ *         is empty, tokens of no row are not written), or NULL: total_tokens /
+ *         batch tokens each (a whole number)
+ * Rows whose new tokens fall into one page slot race (rows share full pages
+ * only: see gdn_pages_fork).  total_tokens is at most 2^28.  batch == 0 or
+ * total_tokens == 0 is a no-op.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int64_t total_tokens;
+  int32_t batch, hkv, d;
+  int32_t io_dtype, cache_dtype;
+  const void* k;
+  int64_t k_stride_token, k_stride_head;
+  const void* v;
+  int64_t v_stride_token, v_stride_head;
+  const int32_t* cu_seqlens;
+  void* k_cache;
+  int64_t kc_stride_page, kc_stride_token, kc_stride_head;
+  void* v_cache;
+  int64_t vc_stride_page, vc_stride_token, vc_stride_head;
+  int32_t n_pages, page_size, max_pages;
+  const int32_t* page_table;
+  int64_t page_table_stride;
+  const int32_t* lens;
+  const float* k_scale;
+  const float* v_scale;
+} gdn_kv_append_args;
+
+gdn_status gdn_kv_append(const gdn_kv_append_args* args, void* stream);
+
+/* ----------------------------------------------------------------------------
+ * gdn_pages_copy -- contents of pages (or of state-pool and conv-state slots)
+ * copied inside one pool: page dst[i] becomes page src[i] for i < n.
+ *
+ * page_bytes bytes at pool + page*page_stride (bytes, any alignment).  Pairs
+ * with an entry outside [0, n_pages), or equal entries, are skipped.  A page
+ * that one pair writes and another reads or writes is undefined behaviour.
+ * n == 0 is a no-op.
+ * ------------------------------------------------------------------------- */
+gdn_status gdn_pages_copy(void* pool, int64_t page_bytes, int64_t page_stride, int32_t n_pages,
+                          const int32_t* src, const int32_t* dst, int64_t n, void* stream);
+
+/* ----------------------------------------------------------------------------
+ * Page tables on the device.  refs[p] is how many holders page p has (table
+ * rows, and whatever else the caller counts); 0 means free.  A row's pages
+ * are its first ceil(lens / page_size) entries.  Free pages are taken lowest
+ * first in row order, so results are determined by the inputs; nothing is
+ * read on the host, and the calls can be captured.
+ *
+ * Inputs page_table, lens, refs; outputs page_table_out, lens_out, refs_out,
+ * which extend, free and compact also take as the inputs themselves (equal
+ * pointers and strides; partial overlaps are not checked); fork reads rows
+ * while it writes others and needs page_table_out and lens_out apart.
+ * workspace: gdn_pages_workspace_size(rows, n_pages) bytes (256-byte aligned;
+ * pages_free needs none); calls that share one must not overlap.
+ * Requirements: n_pages in [1, 2^24], rows at most 2^20, max_pages >= 1, page_size >= 1,
+ * max_pages * page_size at most 2^30, row strides at least max_pages.
+ *
+ *  extend   Row r grows by add[r] tokens (below 0: by none).  A row is served,
+ *           ok[r] = 1, if the new length fits its table row and the pages that
+ *           it and the rows before it need (those that fit their tables) are
+ *           free; a row that needs no page is always served.  Others stay as
+ *           they are, ok[r] = 0.
+ *  fork     Row r becomes what row parent[r] was on entry: its length and
+ *           pages, shared; parent[r] == r keeps it, an entry outside
+ *           [0, rows) leaves it empty and releases its pages.  A part-filled
+ *           last page that others hold too gets its own copy, so that rows
+ *           may append: dst[r] is the fresh page and src[r] the shared one,
+ *           for gdn_pages_copy on each cache (-1 where there is none).  Where
+ *           every holder has the page as its part-filled last one, the lowest
+ *           such row keeps it.  A row for which no page is left ends empty
+ *           (length 0) with its pages released.  Entries past a row's pages
+ *           become -1.
+ *  free     Rows with mask[r] != 0 release their pages and end empty.
+ *  compact  The pages in use (refs > 0; n_live of them) move to the lowest
+ *           page numbers: the i-th page in use at or above n_live moves to
+ *           the i-th free page below it, in every table entry and in refs.
+ *           src[i], dst[i] for i < n_pages / 2 are the moves, for
+ *           gdn_pages_copy (no page is both; -1 past the last).  lens is not
+ *           read and lens_out not written.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t rows, max_pages, n_pages, page_size;
+  const int32_t* page_table;
+  int64_t page_table_stride;
+  const int32_t* lens;
+  const int32_t* refs;      /* [n_pages] */
+  int32_t* page_table_out;
+  int64_t page_table_out_stride;
+  int32_t* lens_out;
+  int32_t* refs_out;
+  void* workspace;
+  size_t workspace_bytes;
+} gdn_pages_args;
+
+size_t gdn_pages_workspace_size(int32_t rows, int32_t n_pages);
+gdn_status gdn_pages_extend(const gdn_pages_args* args, const int32_t* add, int32_t* ok, void* stream);
+gdn_status gdn_pages_fork(const gdn_pages_args* args, const int32_t* parent, int32_t* src, int32_t* dst,
+                          void* stream);
+gdn_status gdn_pages_free(const gdn_pages_args* args, const uint8_t* mask, void* stream);
+gdn_status gdn_pages_compact(const gdn_pages_args* args, int32_t* src, int32_t* dst, int32_t* n_live,
+                             void* stream);
 
 #ifdef __cplusplus
 }
