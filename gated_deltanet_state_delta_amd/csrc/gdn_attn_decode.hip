@@ -5,82 +5,118 @@
 namespace gdn {
 
 // Joins the parts of one (row, head, token): out = sum_s e^{m_s - M} o_s /
-// sum_s e^{m_s - M} l_s.  One workgroup each; D/4 threads read one part's
-// output, the others further parts, added through LDS in a fixed order.
-template <typename IO, int D>
+// sum_s e^{m_s - M} l_s.  Latency-bound: WPR waves take its parts in turn,
+// eight loads in flight each, the weights in the lanes of one wave.  A row's
+// parts: slot 2k + 1 of its first share k, then slots 2k of the shares behind.
+// Four waves a row (joined through LDS) where rows are few and their parts
+// many, one where rows are many.
+template <typename IO, int D, int WPR>
 __global__ void __launch_bounds__(256) attn_join_kernel(AttnParams p) {
-  constexpr int TPD = D / 4, NG = 256 / TPD;
-  __shared__ f4 part[256];
-  __shared__ float wave_m[4], wave_l[4];
-  const int r = blockIdx.x % p.R, bh = blockIdx.x / p.R, h = bh % p.hkv, b = bh / p.hkv;
-  const int len = attn_len(p, b), chunk = attn_chunk(p, len);
-  const int n = max(1, (int)(((int64_t)len + chunk - 1) / chunk));  // parts that were written
-  const int64_t at0 = (int64_t)bh * p.nsplit * p.R + r;             // part s: at0 + s * R
-  const int tid = threadIdx.x;
+  constexpr int V = D < 64 ? 1 : D / 64;  // dimensions of a lane (the first 32 lanes' for D = 32)
+  __shared__ float red[WPR > 1 ? WPR : 1][64 * V];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t id = WPR > 1 ? blockIdx.x : (int64_t)blockIdx.x * 4 + wave;
+  if (id >= (int64_t)p.batch * p.hkv * p.R) return;
+  const int r = (int)(id % p.R), bh = (int)(id / p.R), h = bh % p.hkv, b = bh / p.hkv;
+  const int2 row = p.plan[b];
+  const int k0 = __builtin_amdgcn_readfirstlane(row.x), n = __builtin_amdgcn_readfirstlane(row.y);
+  if (n == 1) return;  // a whole row, finished where it was walked
+  const int d = min(lane * V, D - V);
+  auto part = [&](int s) { return ((int64_t)(s == 0 ? 2 * k0 + 1 : 2 * (k0 + s)) * p.hkv + h) * p.R + r; };
+
   float m = -__builtin_inff();
-  for (int s = tid; s < n; s += 256) m = fmaxf(m, p.part_ml[(at0 + (int64_t)s * p.R) * 2]);
+  for (int s = lane; s < n; s += 64) m = fmaxf(m, p.part_ml[part(s) * 2]);
   for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-  if ((tid & 63) == 0) wave_m[tid >> 6] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(wave_m[0], wave_m[1]), fmaxf(wave_m[2], wave_m[3]));
   const float mu = m == -__builtin_inff() ? 0.f : m;
-  float l = 0.f;
-  for (int s = tid; s < n; s += 256) {
-    const float* ml = p.part_ml + (at0 + (int64_t)s * p.R) * 2;
-    l += ml[1] * exp2_hw(ml[0] - mu);
+  float l = 0.f, acc[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = 0.f;
+  for (int s0 = 0; s0 < n; s0 += 64) {
+    float w = 0.f;
+    if (s0 + lane < n) {
+      const float* ml = p.part_ml + part(s0 + lane) * 2;
+      w = exp2_hw(ml[0] - mu);
+      l += ml[1] * w;
+    }
+    const int top = min(64, n - s0);
+    for (int j = WPR > 1 ? wave : 0; j < top; j += 8 * WPR) {
+      float o[8][V];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float* src = p.part_o + part(s0 + min(j + i * WPR, top - 1)) * D + d;
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[i][v] = src[v];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int at = j + i * WPR;
+        const float e = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w), min(at, 63)));
+        if (at < top)
+#pragma unroll
+          for (int v = 0; v < V; ++v) acc[v] += e * o[i][v];
+      }
+    }
   }
   for (int o = 32; o > 0; o >>= 1) l += __shfl_xor(l, o);
-  if ((tid & 63) == 0) wave_l[tid >> 6] = l;
-
-  const int grp = tid / TPD, d = (tid % TPD) * 4;
-  f4 acc = {0.f, 0.f, 0.f, 0.f};
-  for (int s = grp; s < n; s += NG) {
-    const int64_t at = at0 + (int64_t)s * p.R;
-    const float w = exp2_hw(p.part_ml[at * 2] - mu);
-    const f4 o = *reinterpret_cast<const f4*>(p.part_o + at * D + d);
+  if constexpr (WPR > 1) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] += w * o[i];
+    for (int v = 0; v < V; ++v) red[wave][lane * V + v] = acc[v];
+    __syncthreads();
+    if (wave != 0) return;
+#pragma unroll
+    for (int w = 1; w < WPR; ++w)
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] += red[w][lane * V + v];
   }
-  part[tid] = acc;
-  __syncthreads();
-  if (tid >= TPD) return;
-  l = (wave_l[0] + wave_l[1]) + (wave_l[2] + wave_l[3]);
-#pragma unroll 4
-  for (int i = 1; i < NG; ++i) acc += part[i * TPD + tid];
   const int t = r / p.group, hq = h * p.group + r % p.group;
-  const int64_t row = ((int64_t)b * p.T + t) * p.hq + hq;
-  attn_store<IO>(p, row * D + d, acc, m, l, h);
-  if (p.lse && tid == 0) p.lse[row] = attn_lse(m, l);
+  const int64_t at = ((int64_t)b * p.T + t) * p.hq + hq;
+  if (lane * V < D) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float out = attn_out(acc[v], m, attn_inv(p, m, l, h));
+      if constexpr (sizeof(IO) == 2) ((__bf16*)p.out)[at * D + d + v] = (__bf16)out;
+      else ((float*)p.out)[at * D + d + v] = out;
+    }
+  }
+  if (p.lse && lane == 0) p.lse[at] = attn_lse(m, l);
 }
 
+template <typename IO, int D>
+static void launch_join_d(const AttnParams& p, hipStream_t stream) {
+  const int64_t rows = (int64_t)p.batch * p.hkv * p.R;
+  if (rows <= 1024) hipLaunchKernelGGL((attn_join_kernel<IO, D, 4>), dim3((unsigned)rows), dim3(256), 0, stream, p);
+  else hipLaunchKernelGGL((attn_join_kernel<IO, D, 1>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, p);
+}
 template <typename IO>
 static void launch_join(const AttnParams& p, int d, hipStream_t stream) {
-  const dim3 grid((unsigned)((int64_t)p.batch * p.hkv * p.R));
-  if (d == 32) hipLaunchKernelGGL((attn_join_kernel<IO, 32>), grid, dim3(256), 0, stream, p);
-  else if (d == 64) hipLaunchKernelGGL((attn_join_kernel<IO, 64>), grid, dim3(256), 0, stream, p);
-  else if (d == 128) hipLaunchKernelGGL((attn_join_kernel<IO, 128>), grid, dim3(256), 0, stream, p);
-  else hipLaunchKernelGGL((attn_join_kernel<IO, 256>), grid, dim3(256), 0, stream, p);
+  if (d == 32) launch_join_d<IO, 32>(p, stream);
+  else if (d == 64) launch_join_d<IO, 64>(p, stream);
+  else if (d == 128) launch_join_d<IO, 128>(p, stream);
+  else launch_join_d<IO, 256>(p, stream);
 }
 
-// Ranges per row: enough workgroups to fill 256 CUs several times over if
-// every row is as long as its table allows, none shorter than kMinChunk keys.
-constexpr int kMinChunk = 128, kWorkgroups = 2048;
-static int attn_splits(const gdn_attn_decode_args& a) {
-  const int64_t R = (int64_t)a.T * (a.hq / a.hkv);
-  const int64_t units = (int64_t)a.batch * a.hkv * ((R + 15) / 16);
-  const int64_t cap = (int64_t)a.max_pages * a.page_size;
-  const int64_t most = (cap + kMinChunk - 1) / kMinChunk;
-  int64_t n = (kWorkgroups + units - 1) / units;
-  if (n > most) n = most;
+// Shares of all rows' steps: waves to fill 256 CUs of 4 SIMDs once (each share
+// as large as the next, so that they end together), but no more shares than
+// steps if every row is as long as its table.  0: one wave per row, head and
+// row tile -- tables of one step, and batches of so many rows that finding the
+// shares would cost more than their evenness gives.
+constexpr int kMostRows = 4096;
+static int attn_shares(const gdn_attn_decode_args& a) {
+  const int64_t R = (int64_t)a.T * (a.hq / a.hkv), each = a.hkv * ((R + 15) / 16);  // waves of a share
+  const int64_t cap = (int64_t)a.max_pages * a.page_size, steps = a.batch * ((cap + kStep - 1) / kStep);
+  if (cap <= kStep || a.batch > kMostRows) return 0;
+  const int es = a.cache_dtype == GDN_E4M3 ? 1 : a.io_dtype == GDN_BF16 ? 2 : 4;
+  const int64_t fill = 1024 * attn_occ(es, a.d) / each;
+  const int64_t n = fill < steps ? fill : steps;
   return n < 1 ? 1 : (int)n;
 }
 
 size_t attn_workspace_bytes(const gdn_attn_decode_args& a) {
   if (a.batch <= 0 || a.T <= 0 || a.hkv <= 0 || a.hq < a.hkv || a.d <= 0 || a.max_pages <= 0 || a.page_size <= 0)
     return 0;
-  const int n = attn_splits(a);
-  if (n == 1) return 0;
-  return (size_t)a.batch * a.hq * a.T * n * (a.d + 2) * sizeof(float);
+  const int shares = attn_shares(a);
+  if (shares == 0) return 0;
+  return (2 * (size_t)shares * a.hq * a.T * (a.d + 2) + 2 * (size_t)a.batch) * sizeof(float);
 }
 
 hipError_t launch_attn_decode(const gdn_attn_decode_args& a, hipStream_t stream) {
@@ -117,7 +153,6 @@ hipError_t launch_attn_decode(const gdn_attn_decode_args& a, hipStream_t stream)
   p.n_pages = a.n_pages;
   p.page_size = a.page_size;
   p.cap = a.max_pages * a.page_size;
-  p.min_chunk = kMinChunk;
   // j / page_size for j < 2^31: with s = ceil(log2(page_size)) and
   // mul = ceil(2^(31 + s) / page_size), the error of mul is below 2^s.
   int s = 0;
@@ -125,21 +160,26 @@ hipError_t launch_attn_decode(const gdn_attn_decode_args& a, hipStream_t stream)
   p.page_mul = (uint32_t)((((uint64_t)1 << (31 + s)) + a.page_size - 1) / a.page_size);
   p.page_shift = 31 + s;
   const size_t need = attn_workspace_bytes(a);
-  p.nsplit = 1;
+  p.shares = a.batch;
+  p.plan = nullptr;
   p.part_o = p.part_ml = nullptr;
   if (need > 0 && a.workspace && a.workspace_bytes >= need) {
-    p.nsplit = attn_splits(a);
+    p.shares = attn_shares(a);
+    const size_t parts = 2 * (size_t)p.shares * a.hq * a.T;
     p.part_o = (float*)a.workspace;
-    p.part_ml = p.part_o + (size_t)a.batch * a.hq * a.T * p.nsplit * a.d;
+    p.part_ml = p.part_o + parts * a.d;
+    p.plan = (int2*)(p.part_ml + parts * 2);
   }
-  const int64_t units = (int64_t)p.batch * p.hkv * p.nsplit;
-  const dim3 grid((unsigned)((units + 7) / 8 * 8 * p.ntile));
+  // Workgroups of 4 waves: see the kernel's mapping.
+  const int rtw = p.ntile > 2 ? 4 : p.ntile, nwg = (p.ntile + rtw - 1) / rtw, per = 8 * (4 / rtw);
+  const int64_t units = (int64_t)p.shares * p.hkv;
+  const dim3 grid((unsigned)((units + per - 1) / per * 8 * nwg));
   hipError_t e;
   if (a.cache_dtype == GDN_E4M3)
     e = a.io_dtype == GDN_BF16 ? launch_attn_bf16_e4m3(p, a.d, grid, stream) : launch_attn_f32_e4m3(p, a.d, grid, stream);
   else
     e = a.io_dtype == GDN_BF16 ? launch_attn_bf16(p, a.d, grid, stream) : launch_attn_f32(p, a.d, grid, stream);
-  if (e != hipSuccess || p.nsplit == 1) return e;
+  if (e != hipSuccess || !p.plan) return e;
   if (a.io_dtype == GDN_BF16) launch_join<__bf16>(p, a.d, stream);
   else launch_join<float>(p, a.d, stream);
   return hipGetLastError();

@@ -11,11 +11,15 @@
 // T * hq/hkv query rows of its head only, so the cache's bytes over the HBM
 // rate are the floor; the products run on MFMA mostly to keep the VALU free.
 //
-// Work split: a workgroup of 4 waves takes one (row b, key-value head,
-// 16 query rows, range of keys); its waves take tiles of KT keys in turn and
-// join through LDS at the end.  With more than one range per row, each
-// writes (m, l, unnormalised output) to the workspace and
-// attn_join_kernel joins them in a fixed order.
+// Work split: a wave walks keys of one key-value head for 16 query rows, by
+// itself: no barrier, and no LDS where pages are whole subtiles.  The lengths
+// are known on the device only, so the keys of all rows, laid end to end in
+// steps of 64, are dealt out evenly: each of a fixed number of waves (as many
+// as the card holds at once) finds its share from the lengths and may end one
+// row, take some whole ones and begin another.  Whole rows are finished on
+// the spot; the parts of a row that several waves share go to the workspace
+// as (m, l, unnormalised output) and attn_join_kernel joins them in a fixed
+// order.
 //
 // No LDS and no shuffles between the cache and MFMA.  Both products are
 // taken transposed, so every operand is in the form in which a lane loads
@@ -30,7 +34,7 @@
 //    A lane holds the output of query row x: rescaling by its own factor
 //    needs no exchange.
 // bf16 weights are split into two bf16 terms (high and rest), so P V keeps
-// the weights to 2^-17; the second MFMA is free next to the loads.
+// the weights to 2^-16; the second MFMA is free next to the loads.
 #pragma once
 
 #include "gdn_device.hpp"
@@ -53,36 +57,80 @@ struct AttnParams {
   const int32_t* lens;
   const float* k_scale;
   const float* v_scale;
-  float* part_o;   // [batch * hkv][nsplit][R][D], nsplit > 1 only
-  float* part_ml;  // [batch * hkv][nsplit][R][2]
+  float* part_o;   // [2 * shares][hkv][R][D]; the workspace's arrays are null when each row is one share
+  float* part_ml;  // [2 * shares][hkv][R][2]
+  int2* plan;      // [batch]: a row's first share and how many it lies in
   float scale_log2;
   uint32_t page_mul, page_shift;  // j / page_size = (j * page_mul) >> page_shift
-  int batch, T, hq, hkv, group, R, ntile, n_pages, page_size, cap, nsplit, min_chunk;
+  int batch, T, hq, hkv, group, R, ntile, n_pages, page_size, cap, shares;
 };
 
-// Keys of one range of a row of len tokens: the row's length over nsplit,
-// rounded up to whole tiles of 64, at least min_chunk.
-__device__ __forceinline__ int attn_chunk(const AttnParams& p, int len) {
-  const int c = (((len + p.nsplit - 1) / p.nsplit) + 63) & ~63;
-  return max(c, p.min_chunk);
-}
 __device__ __forceinline__ int attn_len(const AttnParams& p, int b) {
   const int len = p.lens[b];
   return p.n_pages == 0 ? 0 : min(max(len, 0), p.cap);
 }
 
-// Four outputs at element `at`: the weighted sum over the weights' sum.  A
-// row that sees nothing (maximum -inf) is zero.
-template <typename IO>
-__device__ __forceinline__ void attn_store(const AttnParams& p, int64_t at, f4 o, float m, float l, int h) {
-  const float inv = (p.v_scale ? p.v_scale[h] : 1.0f) / l;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = m == -__builtin_inff() ? 0.f : o[i] * inv;
-  if constexpr (sizeof(IO) == 2)
-    *reinterpret_cast<bf4*>((__bf16*)p.out + at) = bf4{(__bf16)o[0], (__bf16)o[1], (__bf16)o[2], (__bf16)o[3]};
-  else
-    *reinterpret_cast<f4*>((float*)p.out + at) = o;
+constexpr int kStep = 64;  // keys; every share is whole steps of a row
+
+// A row's steps; an empty row has one, which writes its zeros.
+__device__ __forceinline__ int attn_steps(int len) { return max(1, (len + kStep - 1) / kStep); }
+
+__device__ __forceinline__ int wave_scan_add_i(int v) {  // inclusive, in lane order
+  v += dpp_i<0x111, 0xF>(0, v);
+  v += dpp_i<0x112, 0xF>(0, v);
+  v += dpp_i<0x114, 0xF>(0, v);
+  v += dpp_i<0x118, 0xF>(0, v);
+  v += dpp_i<0x142, 0xA>(0, v);
+  v += dpp_i<0x143, 0xC>(0, v);
+  return v;
 }
+
+// Steps [at, at + n) of row b and, once they end that row, of the rows behind
+// it; size: steps of a full share.
+struct AttnShare { int b, at, n, size; };
+
+// Share k of `shares` equal ones (the last may be short or empty).  Each lane
+// sums the steps of batch / 64 neighbouring rows; every wave finds the share
+// for itself, without LDS.  All steps together are below 2^31 (checked on the
+// host against the tables' sizes).
+__device__ __forceinline__ AttnShare attn_share(const AttnParams& p, int k, int lane) {
+  AttnShare r;
+  if (!p.plan) {
+    r.b = k;
+    r.at = 0;
+    r.n = r.size = k < p.batch ? attn_steps(attn_len(p, k)) : 0;
+    return r;
+  }
+  const int per = (p.batch + 63) >> 6, i0 = lane * per, i1 = min(p.batch, i0 + per);
+  int mine = 0;
+  for (int i = i0; i < i1; ++i) mine += attn_steps(attn_len(p, i));
+  const int upto = wave_scan_add_i(mine), from = upto - mine;
+  const int all = __builtin_amdgcn_readlane(upto, 63);
+  r.size = (int)(((int64_t)all + p.shares - 1) / p.shares);
+  const int64_t first = (int64_t)k * r.size;
+  r.n = (int)max((int64_t)0, min((int64_t)r.size, all - first));
+  r.b = r.at = 0;
+  if (r.n == 0) return r;
+  const bool here = first >= from && first < upto;
+  int b = i0, at = (int)first - from;
+  if (here)
+    for (;; ++b) {
+      const int n = attn_steps(attn_len(p, b));
+      if (at < n) break;
+      at -= n;
+    }
+  const int src = __builtin_ctzll(__ballot(here));
+  r.b = __builtin_amdgcn_readlane(b, src);
+  r.at = __builtin_amdgcn_readlane(at, src);
+  return r;
+}
+
+// One output: the weighted sum over the weights' sum.  A row that sees nothing
+// (maximum -inf) is zero.
+__device__ __forceinline__ float attn_inv(const AttnParams& p, float m, float l, int h) {
+  return (p.v_scale ? p.v_scale[h] : 1.0f) / l;
+}
+__device__ __forceinline__ float attn_out(float o, float m, float inv) { return m == -__builtin_inff() ? 0.f : o * inv; }
 // Natural log of the weights' sum, from the maximum and sum in units of log2.
 __device__ __forceinline__ float attn_lse(float m, float l) {
   return m == -__builtin_inff() ? m : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
@@ -91,35 +139,43 @@ __device__ __forceinline__ float attn_lse(float m, float l) {
 // N raw bytes of a row piece, as dwords (2 bytes sit in the low half).
 template <int N> struct Raw { uint32_t w[(N + 3) / 4]; };
 
-template <int N>
+// ONCE: a non-temporal load, for data that no other wave reads.
+template <int N, bool ONCE>
 __device__ __forceinline__ Raw<N> raw_buf(__amdgpu_buffer_rsrc_t r, uint32_t voff) {
+  constexpr int aux = ONCE ? 2 : 0;  // the nt bit
   Raw<N> o;
   if constexpr (N == 16) {
-    const u32x4 t = __builtin_amdgcn_raw_buffer_load_b128(r, voff, 0, 0);
+    const u32x4 t = __builtin_amdgcn_raw_buffer_load_b128(r, voff, 0, aux);
     o.w[0] = t[0]; o.w[1] = t[1]; o.w[2] = t[2]; o.w[3] = t[3];
   } else if constexpr (N == 8) {
-    const auto t = __builtin_amdgcn_raw_buffer_load_b64(r, voff, 0, 0);
+    const auto t = __builtin_amdgcn_raw_buffer_load_b64(r, voff, 0, aux);
     o.w[0] = t[0]; o.w[1] = t[1];
   } else if constexpr (N == 4) {
-    o.w[0] = __builtin_amdgcn_raw_buffer_load_b32(r, voff, 0, 0);
+    o.w[0] = __builtin_amdgcn_raw_buffer_load_b32(r, voff, 0, aux);
   } else {
-    o.w[0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, voff, 0, 0);
+    o.w[0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, voff, 0, aux);
   }
   return o;
 }
-template <int N>
+template <bool ONCE, typename V>
+__device__ __forceinline__ V load_as(const char* p) {
+  if constexpr (ONCE) return __builtin_nontemporal_load(reinterpret_cast<const V*>(p));
+  else return *reinterpret_cast<const V*>(p);
+}
+template <int N, bool ONCE>
 __device__ __forceinline__ Raw<N> raw_load(const char* p) {
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
   Raw<N> o;
   if constexpr (N == 16) {
-    const u32x4 t = *reinterpret_cast<const u32x4*>(p);
+    const u32x4 t = load_as<ONCE, u32x4>(p);
     o.w[0] = t[0]; o.w[1] = t[1]; o.w[2] = t[2]; o.w[3] = t[3];
   } else if constexpr (N == 8) {
-    const uint2 t = *reinterpret_cast<const uint2*>(p);
-    o.w[0] = t.x; o.w[1] = t.y;
+    const u32x2 t = load_as<ONCE, u32x2>(p);
+    o.w[0] = t[0]; o.w[1] = t[1];
   } else if constexpr (N == 4) {
-    o.w[0] = *reinterpret_cast<const uint32_t*>(p);
+    o.w[0] = load_as<ONCE, uint32_t>(p);
   } else {
-    o.w[0] = *reinterpret_cast<const uint16_t*>(p);
+    o.w[0] = load_as<ONCE, uint16_t>(p);
   }
   return o;
 }
@@ -135,11 +191,10 @@ __device__ __forceinline__ uint32_t bf_pair(const Raw<N>& r, int i) {
   else return __builtin_bit_cast(uint32_t, (i & 1) ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r.w[i >> 1], 1.0f, true)
                                                    : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r.w[i >> 1], 1.0f, false));
 }
-// Elements 2i and 2i+1 as floats.
-template <typename KE, int N>
+// Elements 2i and 2i+1 of an fp32 piece.
+template <int N>
 __device__ __forceinline__ f2 f_pair(const Raw<N>& r, int i) {
-  if constexpr (sizeof(KE) == 4) return f2{__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1])};
-  else return (i & 1) ? __builtin_amdgcn_cvt_pk_f32_fp8(r.w[i >> 1], true) : __builtin_amdgcn_cvt_pk_f32_fp8(r.w[i >> 1], false);
+  return f2{__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1])};
 }
 
 // Reductions over the four lane groups g of the lanes with one x: the halves
@@ -163,73 +218,116 @@ __device__ __forceinline__ float sum_over_g(float v) {
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// IO: type of q and out, and of the products (bf16 or fp32); KE: cache element.
+// How many waves a SIMD holds and the bytes of K in a wave's tile.  Either
+// way 64 KiB a CU are in flight; fewer and longer streams read HBM faster as
+// long as a wave's own work between its loads is short.  bf16 and fp32 rows of
+// 256 bytes and more: one wave, 8 KiB (64 ragged rows up to 8192 tokens, 8
+// heads of 128, bf16: 172 us; two waves of 4 KiB 175, two of 8 KiB 184, three
+// 193).  Shorter rows, and e4m3 whose conversion is VALU work: two waves, 4
+// KiB (256 rows, 2 heads of 256, e4m3: 110 us; one wave 131, three 122).
+constexpr int attn_occ(int es, int d) { return es > 1 && d >= 128 ? 1 : 2; }
+
+// IO: type of q and out; KE: cache element.  The products are bf16, or fp32
+// for an fp32 cache.  fp32 queries and weights over an e4m3 cache, whose values
+// bf16 holds exactly, enter as three bf16 terms (24 bits): 3 products of 16x16x32
+// instead of 8 of 16x16x4, which are 16 times slower each.
 template <typename IO, typename KE, int D>
 struct AttnCfg {
   static constexpr int ES = sizeof(KE);
-  static constexpr bool BF = sizeof(IO) == 2;
+  static constexpr bool BF = ES < 4;
+  static constexpr int QT = sizeof(IO) == 2 ? 1 : 3, PT = sizeof(IO) == 2 ? 2 : 3;  // bf16 terms of queries, of weights
   static constexpr int kmin(int a, int b) { return a < b ? a : b; }
   static constexpr int KW = kmin(16 / ES, D / 4), NC = D / (4 * KW);    // elements per K piece, pieces per row and lane
   static constexpr int VW = kmin(16 / ES, D / 16), U = D / (16 * VW);   // the same for V
-  // Keys per wave tile: about 8 KiB of K, a multiple of the products' depth.
-  static constexpr int KTW = 8192 / (D * ES);
-  static constexpr int KT = KTW > 64 ? 64 : KTW < (BF ? 32 : 16) ? (BF ? 32 : 16) : KTW;
+  // Keys of a tile, a multiple of the products' depth.
+  static constexpr int OCC = attn_occ(ES, D), KTW = 8192 / OCC / (D * ES);
+  static constexpr int KT = KTW > 64 ? 64 : KTW < 16 ? 16 : KTW;
   static constexpr int NT = KT / 16;
   static constexpr int NA = D / 16;  // accumulator tiles
-  static constexpr int LDO = D + 4;  // row pitch of the join buffer: rows 4 banks apart
 };
 
 // UNI: page_size is a multiple of 16, so every 16-key subtile lies in one
 // page: its base is a scalar and rows past the end read zeros through the
 // buffer's bound.  Otherwise each key's offset is looked up by one lane and
 // passed through LDS.
-template <typename IO, typename KE, int D, bool UNI>
-__global__ void __launch_bounds__(256) attn_decode_kernel(AttnParams p) {
+// KIND 0: one new token and one row tile.  1: several new tokens.  2: several
+// row tiles, whose waves share what they read; in the others no second wave
+// reads a key, and non-temporal loads leave the caches alone (the batch above:
+// 184 us against 201 with ordinary ones, at two waves of 8 KiB).
+template <typename IO, typename KE, int D, bool UNI, int KIND>
+__global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D>::OCC)) attn_decode_kernel(AttnParams p) {
   typedef AttnCfg<IO, KE, D> C;
   constexpr int KT = C::KT, NT = C::NT, NC = C::NC, KW = C::KW, VW = C::VW, U = C::U, NA = C::NA, ES = C::ES;
-  constexpr bool BF = C::BF;
+  constexpr bool BF = C::BF, MT = KIND > 0, ONCE = KIND < 2;
+  constexpr int QT = C::QT, PT = C::PT;
   constexpr uint64_t kNone = ~0ull;
-  __shared__ __align__(16) float red[16 * C::LDO];
-  __shared__ float red_m[4][16], red_l[4][16];
   __shared__ uint64_t offs[UNI ? 1 : 4][2][2][UNI ? 1 : KT];  // [wave][parity][K, V][key]
 
-  const int lane = threadIdx.x & 63, x = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // Workgroup -> (unit, row tile): the row tiles of a unit, which read the
-  // same keys, are 8 apart and so on one XCD (workgroups go round the 8).
-  const int nt8 = p.ntile * 8, blk = blockIdx.x;
-  const int unit = (blk / nt8) * 8 + (blk & 7), rt = (blk % nt8) >> 3;
-  if (unit >= p.batch * p.hkv * p.nsplit) return;
-  const int h = unit % p.hkv, split = (unit / p.hkv) % p.nsplit, b = unit / (p.hkv * p.nsplit);
-  const int len = attn_len(p, b), chunk = attn_chunk(p, len);
-  const int64_t c0l = (int64_t)split * chunk;
-  if (split > 0 && c0l >= len) return;  // the join skips the same ranges
-  const int c0 = (int)c0l, c1 = min(len, c0 + chunk);
+  // Wave -> (share, head, row tile).  A workgroup's waves take the row tiles
+  // of one (share, head), which read the same keys, or neighbouring heads,
+  // whose rows are neighbours in a tokens-first cache; further workgroups of
+  // one (share, head) are 8 apart and so on one XCD (they go round the 8).
+  const int rtw = p.ntile > 2 ? 4 : p.ntile, nwg = (p.ntile + rtw - 1) / rtw;
+  const int unit = (int)((blockIdx.x / (8 * nwg) * 8 + (blockIdx.x & 7)) * (4 / rtw)) + wave / rtw;
+  const int rt = (int)(blockIdx.x / 8 % nwg) * rtw + wave % rtw;
+  const int h = unit % p.hkv, share_id = unit / p.hkv;
+  if (share_id >= p.shares || rt >= p.ntile) return;
+  AttnShare share = attn_share(p, share_id, lane);
 
+  const float s_scale = p.scale_log2 * (p.k_scale ? p.k_scale[h] : 1.0f);
+
+  while (share.n > 0) {
+  const int b = share.b, len = attn_len(p, b), row_steps = attn_steps(len), at = share.at;
+  const int take = min(share.n, row_steps - at);
+  const int c0 = at * kStep, c1 = min(len, (at + take) * kStep);
+  const bool whole = take == row_steps;
+  const int slot = 2 * share_id + (at == 0);  // of a part: one that begins a row, one that does not
+  if (p.plan && at == 0 && h == 0 && rt == 0 && lane == 0)
+    p.plan[b] = make_int2(share_id, 1 + (row_steps - take + share.size - 1) / share.size);
+  share.n -= take;
+  share.b = b + 1;
+  share.at = 0;
+
+  // The lane's place, opaque to the compiler: what follows from it is computed
+  // for each row anew rather than held in registers across the walk.
+  int own = lane;
+  asm volatile("" : "+v"(own));
+  const int x = own & 15, g = own >> 4;
   // This lane's query row: row r is token r / group, query head h*group + r % group.
   const int r = rt * 16 + x;
   const bool row_ok = r < p.R;
   const int t_row = row_ok ? r / p.group : 0, hq_row = h * p.group + (row_ok ? r % p.group : 0);
-  const int lim = row_ok ? max(0, min(len, len - p.T + t_row + 1)) : 0;  // it sees keys below lim
+  const int lim = row_ok ? max(0, min(len, len - p.T + t_row + 1)) : 0;  // the lane's row sees keys below lim
   const char* qp = (const char*)p.q + b * p.q_sb + t_row * p.q_st + hq_row * p.q_sh;
-  const float s_scale = p.scale_log2 * (p.k_scale ? p.k_scale[h] : 1.0f);
-
-  bf8 qb[BF ? D / 32 : 1];
+  bf8 qb[BF ? QT : 1][BF ? D / 32 : 1];
   float qf[BF ? 1 : D / 4];
 #pragma unroll
-  for (int c = 0; c < NC; ++c) {
+  for (int i = 0; i < D / 4; i += BF ? 8 : 4) {
+    const int c = i / KW, d = 4 * KW * c + KW * g + i % KW;
+    if constexpr (BF && sizeof(IO) == 2) {
+      bf8 t = {};
+      if (row_ok) t = *reinterpret_cast<const bf8*>(qp + d * 2);
+      qb[0][i / 8] = t;
+    } else {
 #pragma unroll
-    for (int w = 0; w < KW; w += BF ? 8 : 4) {
-      const int d = 4 * KW * c + KW * g + w, i = (c * KW + w);
-      if constexpr (BF) {
-        bf8 t = {};
-        if (row_ok) t = *reinterpret_cast<const bf8*>(qp + d * 2);
-        qb[i / 8] = t;
-      } else {
+      for (int k = 0; k < (BF ? 8 : 4); k += 4) {
         f4 t = {};
-        if (row_ok) t = *reinterpret_cast<const f4*>(qp + d * 4);
+        if (row_ok) t = *reinterpret_cast<const f4*>(qp + (d + k) * 4);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) qf[i + e] = t[e];
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (BF) {
+            float rest = t[e];
+#pragma unroll
+            for (int n = 0; n < QT; ++n) {
+              qb[n][i / 8][k + e] = (__bf16)rest;
+              rest -= (float)qb[n][i / 8][k + e];
+            }
+          } else {
+            qf[i + e] = t[e];
+          }
+        }
       }
     }
   }
@@ -246,8 +344,8 @@ __global__ void __launch_bounds__(256) attn_decode_kernel(AttnParams p) {
   Raw<KW * ES> kr[NT][NC];
   Raw<VW * ES> vr[NT][4][U];
 
-  const int first = c0 + wave * KT;
-  constexpr int STEP = 4 * KT;
+  const int first = c0;
+  constexpr int STEP = KT;
 
   // ---- page lookups
   auto page_of = [&](int key) -> int { return (int)(((uint64_t)(uint32_t)key * p.page_mul) >> p.page_shift); };
@@ -273,7 +371,7 @@ __global__ void __launch_bounds__(256) attn_decode_kernel(AttnParams p) {
     for (int n = 0; n < NT; ++n) {
       const auto rs = sub_rsrc(kbase, p.k_sp, p.k_st, en.e[n], key0 + 16 * n);
 #pragma unroll
-      for (int c = 0; c < NC; ++c) kr[n][c] = raw_buf<KW * ES>(rs, x * p.k_st + (4 * KW * c + KW * g) * ES);
+      for (int c = 0; c < NC; ++c) kr[n][c] = raw_buf<KW * ES, ONCE>(rs, x * p.k_st + (4 * KW * c + KW * g) * ES);
     }
   };
   auto issue_v_uni = [&](const Ents& en, int key0) {
@@ -284,7 +382,7 @@ __global__ void __launch_bounds__(256) attn_decode_kernel(AttnParams p) {
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          vr[n][j][u] = raw_buf<VW * ES>(rs, (4 * g + j) * p.v_st + (16 * VW * u + VW * x) * ES);
+          vr[n][j][u] = raw_buf<VW * ES, ONCE>(rs, (4 * g + j) * p.v_st + (16 * VW * u + VW * x) * ES);
     }
   };
   // Not UNI: lane l < KT looks up key l of a tile; `publish` leaves the byte
@@ -306,7 +404,7 @@ __global__ void __launch_bounds__(256) attn_decode_kernel(AttnParams p) {
       const uint64_t o = offs[wave][par][0][16 * n + x];
       const char* src = kbase + (o == kNone ? 0 : o);  // no row: any row, masked below
 #pragma unroll
-      for (int c = 0; c < NC; ++c) kr[n][c] = raw_load<KW * ES>(src + (4 * KW * c + KW * g) * ES);
+      for (int c = 0; c < NC; ++c) kr[n][c] = raw_load<KW * ES, ONCE>(src + (4 * KW * c + KW * g) * ES);
     }
   };
   uint32_t held = ~0u;  // bit 4n + j: key 16n + 4g + j has a row
@@ -320,7 +418,7 @@ __global__ void __launch_bounds__(256) attn_decode_kernel(AttnParams p) {
         held |= (o == kNone ? 0u : 1u) << (4 * n + j);
         const char* src = vbase + (o == kNone ? 0 : o);
 #pragma unroll
-        for (int u = 0; u < U; ++u) vr[n][j][u] = raw_load<VW * ES>(src + (16 * VW * u + VW * x) * ES);
+        for (int u = 0; u < U; ++u) vr[n][j][u] = raw_load<VW * ES, ONCE>(src + (16 * VW * u + VW * x) * ES);
       }
   };
 
@@ -355,12 +453,14 @@ __global__ void __launch_bounds__(256) attn_decode_kernel(AttnParams p) {
             u32x4 t;
 #pragma unroll
             for (int i = 0; i < 4; ++i) t[i] = bf_pair<KE>(kr[n][c], w / 2 + i);
-            s[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, t), qb[(c * KW + w) / 8], s[n], 0, 0, 0);
+#pragma unroll
+            for (int k = QT - 1; k >= 0; --k)
+              s[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, t), qb[k][(c * KW + w) / 8], s[n], 0, 0, 0);
           }
         } else {
 #pragma unroll
           for (int i = 0; i < KW / 2; ++i) {
-            const f2 t = f_pair<KE>(kr[n][c], i);
+            const f2 t = f_pair(kr[n][c], i);
             s[n] = __builtin_amdgcn_mfma_f32_16x16x4f32(t[0], qf[c * KW + 2 * i], s[n], 0, 0, 0);
             s[n] = __builtin_amdgcn_mfma_f32_16x16x4f32(t[1], qf[c * KW + 2 * i + 1], s[n], 0, 0, 0);
           }
@@ -430,7 +530,7 @@ __global__ void __launch_bounds__(256) attn_decode_kernel(AttnParams p) {
     // such a value is present, each token takes the product on its own, with
     // the values that it does not see replaced by zeros.
     bool apart = false;
-    if (p.T > 1 && key0 + KT > len - p.T + 1) {
+    if (MT && key0 + KT > len - p.T + 1) {
       bool odd = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -444,7 +544,7 @@ __global__ void __launch_bounds__(256) attn_decode_kernel(AttnParams p) {
                 const uint32_t w = bf_pair<KE>(vr[n][j][u], e);
                 odd |= (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
               } else {
-                const f2 w = f_pair<KE>(vr[n][j][u], e);
+                const f2 w = f_pair(vr[n][j][u], e);
                 odd |= (__float_as_uint(w[0]) & 0x7f800000u) == 0x7f800000u ||
                        (__float_as_uint(w[1]) & 0x7f800000u) == 0x7f800000u;
               }
@@ -452,41 +552,55 @@ __global__ void __launch_bounds__(256) attn_decode_kernel(AttnParams p) {
       apart = __any(odd);
     }
     if constexpr (BF) {
+      constexpr int NP = NT > 1 ? 2 : 1;  // subtiles of one product: 32 keys deep, or 16
 #pragma unroll
-      for (int a = 0; a < NT; a += 2) {
-        bf8 ph, pl;
+      for (int a = 0; a < NT; a += NP) {
+        bf4 pw[PT][NP];  // the weights' bf16 terms, largest first
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float w = s[a + (j >> 2)][j & 3];
-          ph[j] = (__bf16)w;
-          pl[j] = (__bf16)(w - (float)ph[j]);
-        }
+        for (int i = 0; i < NP; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float rest = s[a + i][j];
+#pragma unroll
+            for (int k = 0; k < PT; ++k) {
+              pw[k][i][j] = (__bf16)rest;
+              rest -= (float)pw[k][i][j];
+            }
+          }
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
           for (int e2 = 0; e2 < VW / 2; ++e2) {
-            uint32_t c[8];
+            uint32_t c[4 * NP];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) c[j] = bf_pair<KE>(vr[a + (j >> 2)][j & 3][u], e2);
+            for (int j = 0; j < 4 * NP; ++j) c[j] = bf_pair<KE>(vr[a + (j >> 2)][j & 3][u], e2);
             auto product = [&](const uint32_t* cc, int half, f4 in) {
-              u32x4 t;
+              bf4 t[NP];
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                t[i] = __builtin_amdgcn_perm(cc[2 * i + 1], cc[2 * i], half ? 0x07060302u : 0x05040100u);
-              in = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, t), ph, in, 0, 0, 0);
-              return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, t), pl, in, 0, 0, 0);
+              for (int i = 0; i < NP; ++i) {
+                uint2 w;
+                w.x = __builtin_amdgcn_perm(cc[4 * i + 1], cc[4 * i], half ? 0x07060302u : 0x05040100u);
+                w.y = __builtin_amdgcn_perm(cc[4 * i + 3], cc[4 * i + 2], half ? 0x07060302u : 0x05040100u);
+                t[i] = __builtin_bit_cast(bf4, w);
+              }
+#pragma unroll
+              for (int k = PT - 1; k >= 0; --k) {
+                if constexpr (NP == 2) in = mma_k32(in, t[0], t[1], pw[k][0], pw[k][1]);
+                else in = mma_k16(in, t[0], pw[k][0]);
+              }
+              return in;
             };
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
               f4& o = acc[u * VW + 2 * e2 + half];
-              if (__builtin_expect(!apart, 1)) {
+              if (!MT || !apart) {
                 o = product(c, half, o);
               } else {
                 const f4 in = o;
                 for (int t = 0; t < p.T; ++t) {
-                  uint32_t cz[8];
+                  uint32_t cz[4 * NP];
 #pragma unroll
-                  for (int j = 0; j < 8; ++j)
+                  for (int j = 0; j < 4 * NP; ++j)
                     cz[j] = key0 + 16 * (a + (j >> 2)) + 4 * g + (j & 3) < len - p.T + t + 1 ? c[j] : 0u;
                   const f4 got = product(cz, half, in);
                   if (t == t_row) o = got;
@@ -504,11 +618,11 @@ __global__ void __launch_bounds__(256) attn_decode_kernel(AttnParams p) {
           for (int e2 = 0; e2 < VW / 2; ++e2) {
             f2 c[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) c[j] = f_pair<KE>(vr[n][j][u], e2);
+            for (int j = 0; j < 4; ++j) c[j] = f_pair(vr[n][j][u], e2);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
               f4& o = acc[u * VW + 2 * e2 + half];
-              if (__builtin_expect(!apart, 1)) {
+              if (!MT || !apart) {
                 o = mma_k16(o, f4{c[0][half], c[1][half], c[2][half], c[3][half]}, s[n]);
               } else {
                 const f4 in = o;
@@ -526,70 +640,55 @@ __global__ void __launch_bounds__(256) attn_decode_kernel(AttnParams p) {
     }
   }
 
-  // ---- join the waves: a common maximum, then the outputs added in wave order
+  // ---- results: the lane's query row, VW neighbouring dimensions at a time
   l = sum_over_g(l);
-  if (g == 0) {
-    red_m[wave][x] = m;
-    red_l[wave][x] = l;
+  asm volatile("" : "+v"(own));
+  const int xo = own & 15, go = own >> 4, ro = rt * 16 + xo;
+  if (ro >= p.R) continue;
+  if (!whole) {
+    const int64_t to = ((int64_t)slot * p.hkv + h) * p.R + ro;
+    float* o = p.part_o + to * D + VW * 4 * go;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < VW; e += 2)
+          *reinterpret_cast<f2*>(o + 16 * VW * u + VW * j + e) = f2{acc[u * VW + e][j], acc[u * VW + e + 1][j]};
+    if (go == 0) *reinterpret_cast<f2*>(p.part_ml + to * 2) = f2{m, l};
+    continue;
   }
-  __syncthreads();
-  float M = red_m[0][x];
+  const int64_t row = ((int64_t)b * p.T + ro / p.group) * p.hq + h * p.group + ro % p.group;
+  IO* o = (IO*)p.out + row * D + VW * 4 * go;
+  const float inv = attn_inv(p, m, l, h);
 #pragma unroll
-  for (int w = 1; w < 4; ++w) M = fmaxf(M, red_m[w][x]);
-  const float Mu = M == -__builtin_inff() ? 0.f : M;
-  float L = 0.f;
+  for (int u = 0; u < U; ++u)
 #pragma unroll
-  for (int w = 0; w < 4; ++w) L += red_l[w][x] * exp2_hw(red_m[w][x] - Mu);
-  const float f = exp2_hw(m - Mu);
-  // acc tile u*VW + e, register j: dimension 16 VW u + VW (4g + j) + e of row x
-  for (int w = 0; w < 4; ++w) {
-    if (wave == w) {
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int e = 0; e < VW; ++e) {
-            float* o = &red[x * C::LDO + 16 * VW * u + VW * (4 * g + j) + e];
-            const float add = acc[u * VW + e][j] * f;
-            *o = w == 0 ? add : *o + add;
-          }
-    }
-    __syncthreads();
+      for (int e = 0; e < VW; e += 2) {
+        typedef IO io2 __attribute__((ext_vector_type(2)));
+        *reinterpret_cast<io2*>(o + 16 * VW * u + VW * j + e) =
+            io2{from_f32<IO>(attn_out(acc[u * VW + e][j], m, inv)), from_f32<IO>(attn_out(acc[u * VW + e + 1][j], m, inv))};
+      }
+  if (p.lse && go == 0) p.lse[row] = attn_lse(m, l);
   }
-  // ---- results: row rr of this tile by 16 threads, 4 dimensions at a time
-  if (wave == 0 && g == 0) red_l[0][x] = L, red_m[0][x] = M;
-  __syncthreads();
-  const int rr = threadIdx.x >> 4, ro = rt * 16 + rr;
-  if (ro >= p.R) return;
-  const float Lr = red_l[0][rr], Mr = red_m[0][rr];
-  const int sub = threadIdx.x & 15;
-  if (p.nsplit > 1) {
-    const int64_t at = ((int64_t)(b * p.hkv + h) * p.nsplit + split) * p.R + ro;
-    for (int d = sub * 4; d < D; d += 64)
-      *reinterpret_cast<f4*>(p.part_o + at * D + d) = *reinterpret_cast<const f4*>(&red[rr * C::LDO + d]);
-    if (sub == 0) {
-      p.part_ml[at * 2] = Mr;
-      p.part_ml[at * 2 + 1] = Lr;
-    }
-    return;
-  }
-  const int t_out = ro / p.group, h_out = h * p.group + ro % p.group;
-  const int64_t row = ((int64_t)b * p.T + t_out) * p.hq + h_out;
-  for (int d = sub * 4; d < D; d += 64)
-    attn_store<IO>(p, row * D + d, *reinterpret_cast<const f4*>(&red[rr * C::LDO + d]), Mr, Lr, h);
-  if (p.lse && sub == 0) p.lse[row] = attn_lse(Mr, Lr);
 }
 
 template <typename IO, typename KE>
 hipError_t launch_attn_t(const AttnParams& p, int d, dim3 grid, hipStream_t stream) {
   const bool uni = p.page_size % 16 == 0;
-#define GDN_ATTN_CASE(DD)                                                                                  \
-  case DD:                                                                                                 \
-    if (uni)                                                                                               \
-      hipLaunchKernelGGL((attn_decode_kernel<IO, KE, DD, true>), grid, dim3(256), 0, stream, p);           \
-    else                                                                                                   \
-      hipLaunchKernelGGL((attn_decode_kernel<IO, KE, DD, false>), grid, dim3(256), 0, stream, p);          \
+  const int kind = p.ntile > 1 ? 2 : p.T > 1 ? 1 : 0;
+#define GDN_ATTN_LAUNCH(DD, UNI, KIND) \
+  hipLaunchKernelGGL((attn_decode_kernel<IO, KE, DD, UNI, KIND>), grid, dim3(256), 0, stream, p)
+#define GDN_ATTN_CASE(DD)                                \
+  case DD:                                               \
+    if (uni && kind == 0) GDN_ATTN_LAUNCH(DD, true, 0);  \
+    else if (uni && kind == 1) GDN_ATTN_LAUNCH(DD, true, 1); \
+    else if (uni) GDN_ATTN_LAUNCH(DD, true, 2);          \
+    else if (kind == 0) GDN_ATTN_LAUNCH(DD, false, 0);   \
+    else if (kind == 1) GDN_ATTN_LAUNCH(DD, false, 1);   \
+    else GDN_ATTN_LAUNCH(DD, false, 2);                  \
     break;
   switch (d) {
     GDN_ATTN_CASE(32)
@@ -599,6 +698,7 @@ hipError_t launch_attn_t(const AttnParams& p, int d, dim3 grid, hipStream_t stre
     default: return hipErrorInvalidValue;
   }
 #undef GDN_ATTN_CASE
+#undef GDN_ATTN_LAUNCH
   return hipGetLastError();
 }
 
