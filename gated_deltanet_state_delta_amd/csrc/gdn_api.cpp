@@ -434,7 +434,7 @@ static gdn_status pages_check(const char* f, const gdn_pages_args* p, bool lens,
   if (a.rows < 0 || a.max_pages <= 0 || a.n_pages <= 0 || a.page_size <= 0)
     return fail(GDN_ERR_SHAPE, "%s: bad sizes rows=%d max_pages=%d n_pages=%d page_size=%d", f, a.rows, a.max_pages,
                 a.n_pages, a.page_size);
-  if (a.n_pages > (1 << 24)) return fail(GDN_ERR_UNSUPPORTED, "%s: n_pages=%d (supported up to 2^24)", f, a.n_pages);
+  if (a.n_pages > (1 << 22)) return fail(GDN_ERR_UNSUPPORTED, "%s: n_pages=%d (supported up to 2^22)", f, a.n_pages);
   if (a.rows > (1 << 20)) return fail(GDN_ERR_UNSUPPORTED, "%s: rows=%d (supported up to 2^20)", f, a.rows);
   if ((int64_t)a.max_pages * a.page_size > (int64_t(1) << 30))
     return fail(GDN_ERR_UNSUPPORTED, "%s: max_pages * page_size must be at most 2^30", f);

@@ -8,10 +8,11 @@
 // are padded with -1.
 //
 // The calls are launch-bound at serving sizes (a few MB of tables and
-// counts).  Ranking free pages takes two passes over the counts, tile by
-// tile: every workgroup counts its tile, then every workgroup sums the counts
-// of the tiles before its own and ranks inside it -- no workgroup waits for
-// another inside a launch.
+// counts), so launches are few: extend takes two, compact three, fork four.
+// One pass over the counts leaves each tile's number of free pages and their
+// bits; the workgroup of a row then finds the pages of its ranks by scanning
+// the tiles' numbers and the bits of the tiles that hold them.  No workgroup
+// waits for another inside a launch.
 #include "gdn_device.hpp"
 #include "gdn_kernels.hpp"
 
@@ -76,12 +77,12 @@ struct PagesParams {
   int32_t* refs_out;
   int64_t table_stride, table_out_stride;
   int rows, max_pages, n_pages, page_size, tiles;
-  // workspace: counts of a tile, ranked pages, per row and per page scratch
+  // workspace: per tile, ranked pages, per row and per page scratch
   int32_t* tile_n;
+  uint64_t* bits;  // free pages, 16 words a tile
   int32_t* list;
   int32_t* row_a;
   int32_t* row_b;
-  int32_t* row_c;
   int32_t* page_a;
   int32_t* page_b;
   int32_t* page_c;
@@ -120,19 +121,23 @@ __device__ __forceinline__ int row_len(const PagesParams& p, const int32_t* lens
 __device__ __forceinline__ int pages_of(const PagesParams& p, int len) { return (int)(((int64_t)len + p.page_size - 1) / p.page_size); }
 __device__ __forceinline__ bool is_page(const PagesParams& p, int e) { return e >= 0 && e < p.n_pages; }
 
-// refs -> refs_out, and how many pages of each tile are free.
-// LIVE counts pages in use instead.
+// refs -> refs_out if `copy`, and how many pages of this workgroup's tile are
+// free (LIVE: in use), with their bits.
 template <bool LIVE>
 __device__ __forceinline__ void count_tile(const PagesParams& p, const int32_t* refs, bool copy, int* lds) {
   int n = 0;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int64_t i = (int64_t)blockIdx.x * kTile + k * 256 + threadIdx.x;
+    bool hit = false;
     if (i < p.n_pages) {
       const int v = refs[i];
-      n += LIVE ? v > 0 : v == 0;
+      hit = LIVE ? v > 0 : v == 0;
       if (copy) p.refs_out[i] = v;
     }
+    const uint64_t bits = __ballot(hit);
+    if (!LIVE && (threadIdx.x & 63) == 0) p.bits[(int64_t)blockIdx.x * 16 + k * 4 + (threadIdx.x >> 6)] = bits;
+    n += hit;
   }
   n = block_sum(n, lds);
   if (threadIdx.x == 0) p.tile_n[blockIdx.x] = n;
@@ -148,76 +153,98 @@ __device__ __forceinline__ int tiles_before(const PagesParams& p, int tile, int*
   all = block_sum(t, lds);
   return block_sum(a, lds);
 }
-// The tile's free pages to their ranks in `list`.
-__device__ __forceinline__ void rank_tile(const PagesParams& p, const int32_t* refs, int* lds) {
-  int all;
-  int base = tiles_before(p, blockIdx.x, lds, all);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.total = all;
+
+// Calls use(rank, page) once for each free page whose rank lies in [start,
+// end), in any thread, from the counts and bits that count_tile left.  The
+// whole workgroup calls it; returns the number of free pages up to the last
+// tile that it looked at (all of them where that is at most start).
+struct TileList { int n[256], before[256]; };
+template <typename F>
+__device__ __forceinline__ int free_pages(const PagesParams& p, int start, int end, int* lds, TileList& found, F use) {
+  int base = 0;
+  for (int t0 = 0; t0 < p.tiles && base < end; t0 += 256) {
+    const int t = t0 + threadIdx.x, v = t < p.tiles ? p.tile_n[t] : 0;
+    int all, count;
+    const int before = base + block_before(v, lds, all);
+    const bool holds = v > 0 && before < end && before + v > start;
+    const int at = block_before(holds, lds, count);
+    if (holds) {
+      found.n[at] = t;
+      found.before[at] = before;
+    }
+    __syncthreads();
+    for (int i = 0; i < count; ++i) {
+      const int tile = found.n[i];
+      const uint32_t four = (uint32_t)(p.bits[(int64_t)tile * 16 + (threadIdx.x >> 4)] >> (4 * (threadIdx.x & 15))) & 15u;
+      int unused;
+      int rank = found.before[i] + block_before(__popc(four), lds, unused);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int64_t i = (int64_t)blockIdx.x * kTile + k * 256 + threadIdx.x;
-    const bool f = i < p.n_pages && refs[i] == 0;
-    int n;
-    const int at = block_before(f, lds, n);
-    if (f) p.list[base + at] = (int)i;
-    base += n;
+      for (int k = 0; k < 4; ++k)
+        if ((four >> k) & 1) {
+          if (rank >= start && rank < end) use(rank, tile * kTile + (int)threadIdx.x * 4 + k);
+          ++rank;
+        }
+    }
+    __syncthreads();
+    base += all;
   }
+  return base;
 }
 
 // ----------------------------------------------------------------- extend --
 
-__global__ void __launch_bounds__(256) extend_count_kernel(PagesParams p) {
+// Tiles count their free pages; the last workgroup sums the rows' needs in
+// order: row_a, the pages that the rows before need (at most n_pages + 1), and
+// row_b, the row's own, -1 where it would outgrow its table.
+__global__ void __launch_bounds__(256) extend_count_kernel(PagesParams p, const int32_t* add) {
   __shared__ int lds[4];
-  count_tile<false>(p, p.refs, p.refs_out != p.refs, lds);
-}
-
-// Tiles rank their free pages; the last workgroup walks the rows in order:
-// a row is served if the pages needed up to and with it are there.
-__global__ void __launch_bounds__(256) extend_rank_kernel(PagesParams p, const int32_t* add, int32_t* ok_out) {
-  __shared__ int lds[4];
-  if ((int)blockIdx.x < p.tiles) return rank_tile(p, p.refs, lds);
-  int n_free;
-  tiles_before(p, 0, lds, n_free);
-  int64_t before = 0;  // pages needed by the rows of earlier steps
+  if ((int)blockIdx.x < p.tiles) return count_tile<false>(p, p.refs, p.refs_out != p.refs, lds);
+  int64_t before = 0;
   for (int r0 = 0; r0 < p.rows; r0 += 256) {
     const int r = r0 + threadIdx.x;
-    int len = 0, have = 0, need = 0;
-    int64_t grown = 0;
-    bool fits = false;
+    int need = -1;
     if (r < p.rows) {
-      len = row_len(p, p.lens, r);
-      grown = (int64_t)len + max(add[r], 0);
-      fits = grown <= (int64_t)p.max_pages * p.page_size;
-      have = pages_of(p, len);
-      if (fits) need = pages_of(p, (int)grown) - have;
+      const int len = row_len(p, p.lens, r);
+      const int64_t grown = (int64_t)len + max(add[r], 0);
+      if (grown <= (int64_t)p.max_pages * p.page_size) need = pages_of(p, (int)grown) - pages_of(p, len);
     }
+    // a need counts as n_pages + 1 at most, so that a step's 256 stay below 2^31
     int all;
-    const int at = block_before(need, lds, all);
+    const int at = block_before(min(max(need, 0), p.n_pages + 1), lds, all);
     if (r < p.rows) {
-      const int64_t upto = before + at + need;
-      const bool ok = fits && (need == 0 || upto <= n_free);
-      p.row_a[r] = ok ? (int)(upto - need) : 0;
-      p.row_b[r] = have;
-      p.row_c[r] = ok ? need : 0;
-      ok_out[r] = ok;
-      p.lens_out[r] = ok ? (int)grown : len;
+      p.row_a[r] = (int)min(before + at, (int64_t)p.n_pages + 1);
+      p.row_b[r] = need;
     }
-    before += all;
+    before = min(before + all, (int64_t)p.n_pages + 1);
   }
 }
 
-__global__ void __launch_bounds__(256) extend_assign_kernel(PagesParams p) {
-  const int r = blockIdx.x;
-  const int start = p.row_a[r], have = p.row_b[r], n = p.row_c[r];
+__global__ void __launch_bounds__(256) extend_assign_kernel(PagesParams p, const int32_t* add, int32_t* ok_out) {
+  __shared__ int lds[4];
+  __shared__ TileList found;
+  const int r = blockIdx.x, start = p.row_a[r], need = p.row_b[r];
   const int32_t* from = p.table + r * p.table_stride;
   int32_t* to = p.table_out + r * p.table_out_stride;
-  for (int i = threadIdx.x; i < p.max_pages; i += 256) {
-    int v = from[i];
-    if (i >= have && i < have + n) {
-      v = p.list[start + i - have];
-      p.refs_out[v] = 1;
-    }
-    to[i] = v;
+  const int len = row_len(p, p.lens, r), have = pages_of(p, len);
+  bool ok = need == 0;
+  if (need > 0) {
+    int n_free;
+    tiles_before(p, 0, lds, n_free);
+    ok = start <= n_free - need;  // (start is at most n_pages + 1)
+  }
+  const int n = ok ? need : 0;
+  if (to != from)
+    for (int i = threadIdx.x; i < p.max_pages; i += 256)
+      if (i < have || i >= have + n) to[i] = from[i];
+  if (n > 0)
+    free_pages(p, start, start + n, lds, found, [&](int rank, int page) {
+      to[have + rank - start] = page;
+      p.refs_out[page] = 1;
+    });
+  __syncthreads();  // every thread has read the row's length
+  if (threadIdx.x == 0) {
+    ok_out[r] = ok;
+    p.lens_out[r] = ok ? len + max(add[r], 0) : len;
   }
 }
 
@@ -281,28 +308,32 @@ __global__ void __launch_bounds__(256) fork_count_kernel(PagesParams p) {
   }
 }
 
-__global__ void __launch_bounds__(256) fork_rank_kernel(PagesParams p) {
-  __shared__ int lds[4];
-  rank_tile(p, p.refs_out, lds);
-}
-
 __global__ void __launch_bounds__(256) fork_assign_kernel(PagesParams p, int32_t* src, int32_t* dst) {
+  __shared__ int lds[4], fresh;
+  __shared__ TileList found;
   const int r = blockIdx.x, rank = p.row_a[r];
-  const bool served = rank >= 0 && rank < *p.total;
-  if (rank >= 0 && !served) {  // no page left: the row ends empty
-    int32_t* to = p.table_out + r * p.table_out_stride;
+  int32_t* to = p.table_out + r * p.table_out_stride;
+  if (rank < 0) {
+    if (threadIdx.x == 0) src[r] = dst[r] = -1;
+    return;
+  }
+  if (threadIdx.x == 0) fresh = -1;
+  free_pages(p, rank, rank + 1, lds, found, [&](int, int page) { fresh = page; });
+  __syncthreads();
+  const int d = fresh;
+  if (d < 0) {  // no page left: the row ends empty
     for (int i = threadIdx.x; i < p.max_pages; i += 256) {
       if (is_page(p, to[i])) atomicSub(&p.refs_out[to[i]], 1);
       to[i] = -1;
     }
-    if (threadIdx.x == 0) p.lens_out[r] = 0;
   }
   if (threadIdx.x == 0) {
-    int s = -1, d = -1;
-    if (served) {
-      int32_t* e = p.table_out + r * p.table_out_stride + p.lens_out[r] / p.page_size;
+    int s = -1;
+    if (d < 0) {
+      p.lens_out[r] = 0;
+    } else {
+      int32_t* e = to + p.lens_out[r] / p.page_size;
       s = *e;
-      d = p.list[rank];
       *e = d;
       atomicSub(&p.refs_out[s], 1);
       p.refs_out[d] = 1;
@@ -415,11 +446,11 @@ __global__ void __launch_bounds__(256) compact_apply_kernel(PagesParams p, int32
 
 // ----------------------------------------------------------------- launch --
 
-// Workspace, in int32 words: [total, padded to 64][tile counts][list, page_a,
-// page_b, page_c: n_pages each][row_a, row_b, row_c: rows each].
+// Workspace, in int32 words: [total, padded to 64][bits, 32 a tile][tile
+// counts][list, page_a, page_b, page_c: n_pages each][row_a, row_b: rows each].
 size_t pages_workspace_bytes(int64_t rows, int64_t n_pages) {
   const int64_t tiles = (n_pages + kTile - 1) / kTile;
-  return (size_t)(64 + tiles + 4 * n_pages + 3 * rows) * sizeof(int32_t);
+  return (size_t)(64 + 33 * tiles + 4 * n_pages + 2 * rows) * sizeof(int32_t);
 }
 
 static PagesParams pages_params(const gdn_pages_args& a) {
@@ -438,32 +469,31 @@ static PagesParams pages_params(const gdn_pages_args& a) {
   p.page_size = a.page_size;
   p.tiles = (a.n_pages + kTile - 1) / kTile;
   p.total = (int32_t*)a.workspace;
-  p.tile_n = p.total + 64;
+  p.bits = (uint64_t*)(p.total + 64);
+  p.tile_n = p.total + 64 + 32 * p.tiles;
   p.list = p.tile_n + p.tiles;
   p.page_a = p.list + a.n_pages;
   p.page_b = p.page_a + a.n_pages;
   p.page_c = p.page_b + a.n_pages;
   p.row_a = p.page_c + a.n_pages;
   p.row_b = p.row_a + a.rows;
-  p.row_c = p.row_b + a.rows;
   return p;
 }
 
 hipError_t launch_pages_extend(const gdn_pages_args& a, const int32_t* add, int32_t* ok, hipStream_t stream) {
   const PagesParams p = pages_params(a);
-  hipLaunchKernelGGL(extend_count_kernel, dim3(p.tiles), dim3(256), 0, stream, p);
-  hipLaunchKernelGGL(extend_rank_kernel, dim3(p.tiles + 1), dim3(256), 0, stream, p, add, ok);
-  if (p.rows > 0) hipLaunchKernelGGL(extend_assign_kernel, dim3(p.rows), dim3(256), 0, stream, p);
+  hipLaunchKernelGGL(extend_count_kernel, dim3(p.tiles + 1), dim3(256), 0, stream, p, add);
+  if (p.rows > 0) hipLaunchKernelGGL(extend_assign_kernel, dim3(p.rows), dim3(256), 0, stream, p, add, ok);
   return hipGetLastError();
 }
 
 hipError_t launch_pages_fork(const gdn_pages_args& a, const int32_t* parent, int32_t* src, int32_t* dst, hipStream_t stream) {
   const PagesParams p = pages_params(a);
   hipLaunchKernelGGL(fork_init_kernel, dim3((p.n_pages + 255) / 256), dim3(256), 0, stream, p);
-  if (p.rows > 0) hipLaunchKernelGGL(fork_rows_kernel, dim3(p.rows), dim3(256), 0, stream, p, parent);
+  if (p.rows == 0) return hipGetLastError();
+  hipLaunchKernelGGL(fork_rows_kernel, dim3(p.rows), dim3(256), 0, stream, p, parent);
   hipLaunchKernelGGL(fork_count_kernel, dim3(p.tiles + 1), dim3(256), 0, stream, p);
-  hipLaunchKernelGGL(fork_rank_kernel, dim3(p.tiles), dim3(256), 0, stream, p);
-  if (p.rows > 0) hipLaunchKernelGGL(fork_assign_kernel, dim3(p.rows), dim3(256), 0, stream, p, src, dst);
+  hipLaunchKernelGGL(fork_assign_kernel, dim3(p.rows), dim3(256), 0, stream, p, src, dst);
   return hipGetLastError();
 }
 

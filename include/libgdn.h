@@ -555,7 +555,7 @@ gdn_status gdn_pages_copy(void* pool, int64_t page_bytes, int64_t page_stride, i
  * while it writes others and needs page_table_out and lens_out apart.
  * workspace: gdn_pages_workspace_size(rows, n_pages) bytes (256-byte aligned;
  * pages_free needs none); calls that share one must not overlap.
- * Requirements: n_pages in [1, 2^24], rows at most 2^20, max_pages >= 1, page_size >= 1,
+ * Requirements: n_pages in [1, 2^22], rows at most 2^20, max_pages >= 1, page_size >= 1,
  * max_pages * page_size at most 2^30, row strides at least max_pages.
  *
  *  extend   Row r grows by add[r] tokens (below 0: by none).  A row is served,
