@@ -269,9 +269,12 @@ __global__ void __launch_bounds__(256) fork_rows_kernel(PagesParams p, const int
   for (int i = threadIdx.x; i < p.max_pages; i += 256) {
     const int v = i < used ? src[i] : -1;
     to[i] = v;
-    if (from == r) continue;  // keeps what it holds
+    // An entry that stays changes no count: a kept row's, and the prompt that
+    // forked rows share, whose pages would draw many atomics to one address.
+    const int had = i < was ? old[i] : -1;
+    if (had == v) continue;
     if (is_page(p, v)) atomicAdd(&p.refs_out[v], 1);
-    if (i < was && is_page(p, old[i])) atomicSub(&p.refs_out[old[i]], 1);
+    if (is_page(p, had)) atomicSub(&p.refs_out[had], 1);
   }
   if (threadIdx.x == 0) {
     p.lens_out[r] = len;
@@ -393,24 +396,29 @@ __global__ void __launch_bounds__(256) compact_rank_kernel(PagesParams p) {
     }
     front += block_sum(n, lds);
   }
+  const int i0 = blockIdx.x * kTile + threadIdx.x * 4;  // four neighbouring pages a thread
+  int v[4], mine = 0, unused;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int64_t i = (int64_t)blockIdx.x * kTile + k * 256 + threadIdx.x;
-    const int v = i < p.n_pages ? p.refs[i] : 0;
-    int n;
-    const int rank = base + block_before(v > 0, lds, n);  // used pages before page i
+    v[k] = i0 + k < p.n_pages ? p.refs[i0 + k] : 0;
+    mine += v[k] > 0;
+  }
+  int rank = base + block_before(mine, lds, unused);  // used pages before page i
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int i = i0 + k;
     if (i < p.n_pages) {
       if (i < n_live) {
-        if (v <= 0) p.list[i - rank] = (int)i;
+        if (v[k] <= 0) p.list[i - rank] = i;
       } else {
-        p.page_a[i] = v > 0 ? rank - front : -1;
-        if (v > 0) {
-          p.page_b[rank - front] = (int)i;
-          p.page_c[rank - front] = v;
+        p.page_a[i] = v[k] > 0 ? rank - front : -1;
+        if (v[k] > 0) {
+          p.page_b[rank - front] = i;
+          p.page_c[rank - front] = v[k];
         }
       }
     }
-    base += n;
+    rank += v[k] > 0;
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) p.total[1] = n_live - front;  // pages that move
 }
