@@ -101,12 +101,17 @@ static void launch_join(const AttnParams& p, int d, hipStream_t stream) {
 // row tile -- tables of one step, and batches of so many rows that finding the
 // shares would cost more than their evenness gives.
 constexpr int kMostRows = 4096;
+// Row tiles (see attn_rows16) of a key-value head.
+static int attn_tiles(const gdn_attn_decode_args& a) {
+  const int R = a.T * (a.hq / a.hkv), rows = 16 * attn_rows16(attn_kind(a.T, R), a.d, a.io_dtype == GDN_BF16 ? 2 : 4);
+  return (R + rows - 1) / rows;
+}
 static int attn_shares(const gdn_attn_decode_args& a) {
-  const int64_t R = (int64_t)a.T * (a.hq / a.hkv), each = a.hkv * ((R + 15) / 16);  // waves of a share
   const int64_t cap = (int64_t)a.max_pages * a.page_size, steps = a.batch * ((cap + kStep - 1) / kStep);
   if (cap <= kStep || a.batch > kMostRows) return 0;
   const int es = a.cache_dtype == GDN_E4M3 ? 1 : a.io_dtype == GDN_BF16 ? 2 : 4;
-  const int64_t fill = 1024 * attn_occ(es, a.d) / each;
+  const int64_t each = (int64_t)a.hkv * attn_tiles(a);  // waves of a share
+  const int64_t fill = 1024 * attn_waves(es, a.d, attn_kind(a.T, a.T * (a.hq / a.hkv))) / each;
   const int64_t n = fill < steps ? fill : steps;
   return n < 1 ? 1 : (int)n;
 }
@@ -149,7 +154,7 @@ hipError_t launch_attn_decode(const gdn_attn_decode_args& a, hipStream_t stream)
   p.hkv = a.hkv;
   p.group = a.hq / a.hkv;
   p.R = a.T * p.group;
-  p.ntile = (p.R + 15) / 16;
+  p.ntile = attn_tiles(a);
   p.n_pages = a.n_pages;
   p.page_size = a.page_size;
   p.cap = a.max_pages * a.page_size;

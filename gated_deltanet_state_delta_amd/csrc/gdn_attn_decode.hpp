@@ -231,7 +231,20 @@ constexpr int attn_occ(int es, int d) { return es > 1 && d >= 128 ? 1 : 2; }
 // for an fp32 cache.  fp32 queries and weights over an e4m3 cache, whose values
 // bf16 holds exactly, enter as three bf16 terms (24 bits): 3 products of 16x16x32
 // instead of 8 of 16x16x4, which are 16 times slower each.
-template <typename IO, typename KE, int D>
+//
+// KIND 0: one new token, up to 16 query rows of a key-value head.  1: several
+// new tokens, up to 16 rows.  2: up to 32 rows.  3: more.
+constexpr int attn_kind(int T, int R) { return R > 32 ? 3 : R > 16 ? 2 : T > 1 ? 1 : 0; }
+// Tiles of 16 query rows of a wave, which reads a key once for all of them: two
+// where the registers hold them (io: bytes of an element of q), one for fp32
+// heads of 256.  64 rows (16 batch rows up to 8192 tokens, 8 heads of 128, bf16):
+// 87 us, with four tiles 95, with one 108.
+constexpr int attn_rows16(int kind, int d, int io) { return kind < 2 || (io == 4 && d > 128) ? 1 : 2; }
+// Waves of a SIMD; with two row tiles a wave needs more than half of its
+// registers from heads of 128 on.
+constexpr int attn_waves(int es, int d, int kind) { return kind > 1 ? d > 64 ? 1 : 2 : attn_occ(es, d); }
+
+template <typename IO, typename KE, int D, int KIND>
 struct AttnCfg {
   static constexpr int ES = sizeof(KE);
   static constexpr bool BF = ES < 4;
@@ -240,7 +253,7 @@ struct AttnCfg {
   static constexpr int KW = kmin(16 / ES, D / 4), NC = D / (4 * KW);    // elements per K piece, pieces per row and lane
   static constexpr int VW = kmin(16 / ES, D / 16), U = D / (16 * VW);   // the same for V
   // Keys of a tile, a multiple of the products' depth.
-  static constexpr int OCC = attn_occ(ES, D), KTW = 8192 / OCC / (D * ES);
+  static constexpr int OCC = attn_waves(ES, D, KIND), KTW = 8192 / attn_occ(ES, D) / (D * ES);
   static constexpr int KT = KTW > 64 ? 64 : KTW < 16 ? 16 : KTW;
   static constexpr int NT = KT / 16;
   static constexpr int NA = D / 16;  // accumulator tiles
@@ -250,22 +263,20 @@ struct AttnCfg {
 // page: its base is a scalar and rows past the end read zeros through the
 // buffer's bound.  Otherwise each key's offset is looked up by one lane and
 // passed through LDS.
-// KIND 0: one new token and one row tile.  1: several new tokens.  2: several
-// row tiles, whose waves share what they read; in the others no second wave
-// reads a key, and non-temporal loads leave the caches alone (the batch above:
-// 184 us against 201 with ordinary ones, at two waves of 8 KiB).
 template <typename IO, typename KE, int D, bool UNI, int KIND>
-__global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D>::OCC)) attn_decode_kernel(AttnParams p) {
-  typedef AttnCfg<IO, KE, D> C;
+__global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND>::OCC)) attn_decode_kernel(AttnParams p) {
+  typedef AttnCfg<IO, KE, D, KIND> C;
   constexpr int KT = C::KT, NT = C::NT, NC = C::NC, KW = C::KW, VW = C::VW, U = C::U, NA = C::NA, ES = C::ES;
-  constexpr bool BF = C::BF, MT = KIND > 0, ONCE = KIND < 2;
-  constexpr int QT = C::QT, PT = C::PT;
+  constexpr int QT = C::QT, PT = C::PT, RT = attn_rows16(KIND, D, sizeof(IO));
+  // Where no second wave reads a key, non-temporal loads leave the caches alone
+  // (the batch above, at two waves of 8 KiB: 184 us against 201 with ordinary ones).
+  constexpr bool BF = C::BF, MT = KIND > 0, ONCE = KIND < 2 || (KIND == 2 && RT == 2);
   constexpr uint64_t kNone = ~0ull;
   __shared__ uint64_t offs[UNI ? 1 : 4][2][2][UNI ? 1 : KT];  // [wave][parity][K, V][key]
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // Wave -> (share, head, row tile).  A workgroup's waves take the row tiles
+  // Wave -> (share, head, row tile of 16 RT rows).  A workgroup's waves take the row tiles
   // of one (share, head), which read the same keys, or neighbouring heads,
   // whose rows are neighbours in a tokens-first cache; further workgroups of
   // one (share, head) are 8 apart and so on one XCD (they go round the 8).
@@ -295,37 +306,43 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D>::OCC)) attn_decode_ke
   int own = lane;
   asm volatile("" : "+v"(own));
   const int x = own & 15, g = own >> 4;
-  // This lane's query row: row r is token r / group, query head h*group + r % group.
-  const int r = rt * 16 + x;
-  const bool row_ok = r < p.R;
-  const int t_row = row_ok ? r / p.group : 0, hq_row = h * p.group + (row_ok ? r % p.group : 0);
-  const int lim = row_ok ? max(0, min(len, len - p.T + t_row + 1)) : 0;  // the lane's row sees keys below lim
-  const char* qp = (const char*)p.q + b * p.q_sb + t_row * p.q_st + hq_row * p.q_sh;
-  bf8 qb[BF ? QT : 1][BF ? D / 32 : 1];
-  float qf[BF ? 1 : D / 4];
+  // This lane's query rows, one of each 16: row r is token r / group, query
+  // head h*group + r % group, and sees keys below lim.
+  int lim[RT], t_row[RT];
+  bf8 qb[RT][BF ? QT : 1][BF ? D / 32 : 1];
+  float qf[RT][BF ? 1 : D / 4];
 #pragma unroll
-  for (int i = 0; i < D / 4; i += BF ? 8 : 4) {
-    const int c = i / KW, d = 4 * KW * c + KW * g + i % KW;
-    if constexpr (BF && sizeof(IO) == 2) {
-      bf8 t = {};
-      if (row_ok) t = *reinterpret_cast<const bf8*>(qp + d * 2);
-      qb[0][i / 8] = t;
-    } else {
+  for (int q = 0; q < RT; ++q) {
+    const int r = (rt * RT + q) * 16 + x;
+    const bool row_ok = r < p.R;
+    t_row[q] = row_ok ? r / p.group : 0;
+    const int hq_row = h * p.group + (row_ok ? r % p.group : 0);
+    lim[q] = row_ok ? max(0, min(len, len - p.T + t_row[q] + 1)) : 0;
+    const char* qp = (const char*)p.q + b * p.q_sb + t_row[q] * p.q_st + hq_row * p.q_sh;
 #pragma unroll
-      for (int k = 0; k < (BF ? 8 : 4); k += 4) {
-        f4 t = {};
-        if (row_ok) t = *reinterpret_cast<const f4*>(qp + (d + k) * 4);
+    for (int i = 0; i < D / 4; i += BF ? 8 : 4) {
+      const int c = i / KW, d = 4 * KW * c + KW * g + i % KW;
+      if constexpr (BF && sizeof(IO) == 2) {
+        bf8 t = {};
+        if (row_ok) t = *reinterpret_cast<const bf8*>(qp + d * 2);
+        qb[q][0][i / 8] = t;
+      } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if constexpr (BF) {
-            float rest = t[e];
+        for (int k = 0; k < (BF ? 8 : 4); k += 4) {
+          f4 t = {};
+          if (row_ok) t = *reinterpret_cast<const f4*>(qp + (d + k) * 4);
 #pragma unroll
-            for (int n = 0; n < QT; ++n) {
-              qb[n][i / 8][k + e] = (__bf16)rest;
-              rest -= (float)qb[n][i / 8][k + e];
+          for (int e = 0; e < 4; ++e) {
+            if constexpr (BF) {
+              float rest = t[e];
+#pragma unroll
+              for (int n = 0; n < QT; ++n) {
+                qb[q][n][i / 8][k + e] = (__bf16)rest;
+                rest -= (float)qb[q][n][i / 8][k + e];
+              }
+            } else {
+              qf[q][i + e] = t[e];
             }
-          } else {
-            qf[i + e] = t[e];
           }
         }
       }
@@ -336,10 +353,15 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D>::OCC)) attn_decode_ke
   const char* vbase = (const char*)p.v + h * p.v_sh;
   const int32_t* tab = p.table + b * p.table_stride;
 
-  f4 acc[NA];
+  f4 acc[RT][NA];
+  float m[RT], l[RT];
 #pragma unroll
-  for (int i = 0; i < NA; ++i) acc[i] = f4{0.f, 0.f, 0.f, 0.f};
-  float m = -__builtin_inff(), l = 0.f;
+  for (int q = 0; q < RT; ++q) {
+#pragma unroll
+    for (int i = 0; i < NA; ++i) acc[q][i] = f4{0.f, 0.f, 0.f, 0.f};
+    m[q] = -__builtin_inff();
+    l[q] = 0.f;
+  }
 
   Raw<KW * ES> kr[NT][NC];
   Raw<VW * ES> vr[NT][4][U];
@@ -441,10 +463,11 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D>::OCC)) attn_decode_ke
     else issue_v_any(par);
 
     // ---- scores of the tile
-    f4 s[NT];
+    f4 s[RT][NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      s[n] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < RT; ++q) s[q][n] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         if constexpr (BF) {
@@ -455,14 +478,20 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D>::OCC)) attn_decode_ke
             for (int i = 0; i < 4; ++i) t[i] = bf_pair<KE>(kr[n][c], w / 2 + i);
 #pragma unroll
             for (int k = QT - 1; k >= 0; --k)
-              s[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, t), qb[k][(c * KW + w) / 8], s[n], 0, 0, 0);
+#pragma unroll
+              for (int q = 0; q < RT; ++q)
+                s[q][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, t), qb[q][k][(c * KW + w) / 8],
+                                                                  s[q][n], 0, 0, 0);
           }
         } else {
 #pragma unroll
           for (int i = 0; i < KW / 2; ++i) {
             const f2 t = f_pair(kr[n][c], i);
-            s[n] = __builtin_amdgcn_mfma_f32_16x16x4f32(t[0], qf[c * KW + 2 * i], s[n], 0, 0, 0);
-            s[n] = __builtin_amdgcn_mfma_f32_16x16x4f32(t[1], qf[c * KW + 2 * i + 1], s[n], 0, 0, 0);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int q = 0; q < RT; ++q)
+                s[q][n] = __builtin_amdgcn_mfma_f32_16x16x4f32(t[e], qf[q][c * KW + 2 * i + e], s[q][n], 0, 0, 0);
           }
         }
       }
@@ -486,34 +515,37 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D>::OCC)) attn_decode_ke
     }
 
     // ---- masks, running maximum, weights
-    float mx = m;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int q = 0; q < RT; ++q) {
+      float mx = m[q];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int key = key0 + 16 * n + 4 * g + j;
-        const bool sees = key < lim && (UNI ? ((sub_ok >> n) & 1) != 0 : ((held >> (4 * n + j)) & 1) != 0);
-        s[n][j] = sees ? s[n][j] * s_scale : -__builtin_inff();
-        mx = fmaxf(mx, s[n][j]);
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int key = key0 + 16 * n + 4 * g + j;
+          const bool sees = key < lim[q] && (UNI ? ((sub_ok >> n) & 1) != 0 : ((held >> (4 * n + j)) & 1) != 0);
+          s[q][n][j] = sees ? s[q][n][j] * s_scale : -__builtin_inff();
+          mx = fmaxf(mx, s[q][n][j]);
+        }
+      mx = max_over_g(mx);
+      const float mu = mx == -__builtin_inff() ? 0.f : mx;
+      const float alpha = exp2_hw(m[q] - mu);
+      if (__any(mx != m[q])) {
+        l[q] *= alpha;
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[q][i][j] *= alpha;
       }
-    mx = max_over_g(mx);
-    const float mu = mx == -__builtin_inff() ? 0.f : mx;
-    const float alpha = exp2_hw(m - mu);
-    if (__any(mx != m)) {
-      l *= alpha;
+      m[q] = mx;
 #pragma unroll
-      for (int i = 0; i < NA; ++i)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] *= alpha;
+        for (int j = 0; j < 4; ++j) {
+          s[q][n][j] = exp2_hw(s[q][n][j] - mu);
+          l[q] += s[q][n][j];
+        }
     }
-    m = mx;
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        s[n][j] = exp2_hw(s[n][j] - mu);
-        l += s[n][j];
-      }
     if constexpr (!UNI) {  // a row that is not there must not reach the product
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -555,18 +587,20 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D>::OCC)) attn_decode_ke
       constexpr int NP = NT > 1 ? 2 : 1;  // subtiles of one product: 32 keys deep, or 16
 #pragma unroll
       for (int a = 0; a < NT; a += NP) {
-        bf4 pw[PT][NP];  // the weights' bf16 terms, largest first
+        bf4 pw[RT][PT][NP];  // the weights' bf16 terms, largest first
 #pragma unroll
-        for (int i = 0; i < NP; ++i)
+        for (int q = 0; q < RT; ++q)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float rest = s[a + i][j];
+          for (int i = 0; i < NP; ++i)
 #pragma unroll
-            for (int k = 0; k < PT; ++k) {
-              pw[k][i][j] = (__bf16)rest;
-              rest -= (float)pw[k][i][j];
+            for (int j = 0; j < 4; ++j) {
+              float rest = s[q][a + i][j];
+#pragma unroll
+              for (int k = 0; k < PT; ++k) {
+                pw[q][k][i][j] = (__bf16)rest;
+                rest -= (float)pw[q][k][i][j];
+              }
             }
-          }
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -574,8 +608,8 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D>::OCC)) attn_decode_ke
             uint32_t c[4 * NP];
 #pragma unroll
             for (int j = 0; j < 4 * NP; ++j) c[j] = bf_pair<KE>(vr[a + (j >> 2)][j & 3][u], e2);
-            auto product = [&](const uint32_t* cc, int half, f4 in) {
-              bf4 t[NP];
+            // V^T's operand for the pieces' lower or upper elements
+            auto dims = [&](const uint32_t* cc, int half, bf4* t) {
 #pragma unroll
               for (int i = 0; i < NP; ++i) {
                 uint2 w;
@@ -583,29 +617,44 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D>::OCC)) attn_decode_ke
                 w.y = __builtin_amdgcn_perm(cc[4 * i + 3], cc[4 * i + 2], half ? 0x07060302u : 0x05040100u);
                 t[i] = __builtin_bit_cast(bf4, w);
               }
-#pragma unroll
-              for (int k = PT - 1; k >= 0; --k) {
-                if constexpr (NP == 2) in = mma_k32(in, t[0], t[1], pw[k][0], pw[k][1]);
-                else in = mma_k16(in, t[0], pw[k][0]);
-              }
-              return in;
             };
+            auto product = [&](const bf4* t, int q, int k, f4 in) {
+              if constexpr (NP == 2) return mma_k32(in, t[0], t[1], pw[q][k][0], pw[q][k][1]);
+              else return mma_k16(in, t[0], pw[q][k][0]);
+            };
+            if (!MT || !apart) {
+              bf4 t[2][NP];
+              dims(c, 0, t[0]);
+              dims(c, 1, t[1]);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              f4& o = acc[u * VW + 2 * e2 + half];
-              if (!MT || !apart) {
-                o = product(c, half, o);
-              } else {
-                const f4 in = o;
-                for (int t = 0; t < p.T; ++t) {
-                  uint32_t cz[4 * NP];
+              for (int k = PT - 1; k >= 0; --k)  // the terms outside: neighbouring products are independent
 #pragma unroll
-                  for (int j = 0; j < 4 * NP; ++j)
-                    cz[j] = key0 + 16 * (a + (j >> 2)) + 4 * g + (j & 3) < len - p.T + t + 1 ? c[j] : 0u;
-                  const f4 got = product(cz, half, in);
-                  if (t == t_row) o = got;
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                  for (int q = 0; q < RT; ++q) {
+                    f4& o = acc[q][u * VW + 2 * e2 + half];
+                    o = product(t[half], q, k, o);
+                  }
+            } else {
+#pragma unroll
+              for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int q = 0; q < RT; ++q) {
+                  f4& o = acc[q][u * VW + 2 * e2 + half];
+                  const f4 in = o;
+                  for (int t = 0; t < p.T; ++t) {
+                    uint32_t cz[4 * NP];
+#pragma unroll
+                    for (int j = 0; j < 4 * NP; ++j)
+                      cz[j] = key0 + 16 * (a + (j >> 2)) + 4 * g + (j & 3) < len - p.T + t + 1 ? c[j] : 0u;
+                    bf4 tz[NP];
+                    dims(cz, half, tz);
+                    f4 got = in;
+#pragma unroll
+                    for (int k = PT - 1; k >= 0; --k) got = product(tz, q, k, got);
+                    if (t == t_row[q]) o = got;
+                  }
                 }
-              }
             }
           }
       }
@@ -620,75 +669,92 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D>::OCC)) attn_decode_ke
 #pragma unroll
             for (int j = 0; j < 4; ++j) c[j] = f_pair(vr[n][j][u], e2);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              f4& o = acc[u * VW + 2 * e2 + half];
-              if (!MT || !apart) {
-                o = mma_k16(o, f4{c[0][half], c[1][half], c[2][half], c[3][half]}, s[n]);
-              } else {
-                const f4 in = o;
-                for (int t = 0; t < p.T; ++t) {
-                  f4 z;
+            for (int half = 0; half < 2; ++half)
 #pragma unroll
-                  for (int j = 0; j < 4; ++j)
-                    z[j] = key0 + 16 * n + 4 * g + j < len - p.T + t + 1 ? c[j][half] : 0.f;
-                  const f4 got = mma_k16(in, z, s[n]);
-                  if (t == t_row) o = got;
+              for (int q = 0; q < RT; ++q) {
+                f4& o = acc[q][u * VW + 2 * e2 + half];
+                if (!MT || !apart) {
+                  o = mma_k16(o, f4{c[0][half], c[1][half], c[2][half], c[3][half]}, s[q][n]);
+                } else {
+                  const f4 in = o;
+                  for (int t = 0; t < p.T; ++t) {
+                    f4 z;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                      z[j] = key0 + 16 * n + 4 * g + j < len - p.T + t + 1 ? c[j][half] : 0.f;
+                    const f4 got = mma_k16(in, z, s[q][n]);
+                    if (t == t_row[q]) o = got;
+                  }
                 }
               }
-            }
           }
     }
   }
 
-  // ---- results: the lane's query row, VW neighbouring dimensions at a time
-  l = sum_over_g(l);
+  // ---- results: the lane's query rows, VW neighbouring dimensions at a time
   asm volatile("" : "+v"(own));
-  const int xo = own & 15, go = own >> 4, ro = rt * 16 + xo;
-  if (ro >= p.R) continue;
-  if (!whole) {
-    const int64_t to = ((int64_t)slot * p.hkv + h) * p.R + ro;
-    float* o = p.part_o + to * D + VW * 4 * go;
+  const int xo = own & 15, go = own >> 4;
+  constexpr int SW = VW < 4 ? VW : 4;
+  typedef float fs __attribute__((ext_vector_type(SW)));
+  typedef IO ios __attribute__((ext_vector_type(SW)));
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+  for (int q = 0; q < RT; ++q) {
+    const float lq = sum_over_g(l[q]);
+    const int ro = (rt * RT + q) * 16 + xo;
+    if (ro < p.R && !whole) {
+      const int64_t to = ((int64_t)slot * p.hkv + h) * p.R + ro;
+      float* o = p.part_o + to * D + VW * 4 * go;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int e = 0; e < VW; e += 2)
-          *reinterpret_cast<f2*>(o + 16 * VW * u + VW * j + e) = f2{acc[u * VW + e][j], acc[u * VW + e + 1][j]};
-    if (go == 0) *reinterpret_cast<f2*>(p.part_ml + to * 2) = f2{m, l};
-    continue;
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < VW; e += SW) {
+            fs w;
+#pragma unroll
+            for (int i = 0; i < SW; ++i) w[i] = acc[q][u * VW + e + i][j];
+            *reinterpret_cast<fs*>(o + 16 * VW * u + VW * j + e) = w;
+          }
+      if (go == 0) *reinterpret_cast<f2*>(p.part_ml + to * 2) = f2{m[q], lq};
+    } else if (ro < p.R) {
+      const int64_t row = ((int64_t)b * p.T + ro / p.group) * p.hq + h * p.group + ro % p.group;
+      IO* o = (IO*)p.out + row * D + VW * 4 * go;
+      const float inv = attn_inv(p, m[q], lq, h);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < VW; e += SW) {
+            ios w;
+#pragma unroll
+            for (int i = 0; i < SW; ++i) w[i] = from_f32<IO>(attn_out(acc[q][u * VW + e + i][j], m[q], inv));
+            *reinterpret_cast<ios*>(o + 16 * VW * u + VW * j + e) = w;
+          }
+      if (p.lse && go == 0) p.lse[row] = attn_lse(m[q], lq);
+    }
   }
-  const int64_t row = ((int64_t)b * p.T + ro / p.group) * p.hq + h * p.group + ro % p.group;
-  IO* o = (IO*)p.out + row * D + VW * 4 * go;
-  const float inv = attn_inv(p, m, l, h);
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int e = 0; e < VW; e += 2) {
-        typedef IO io2 __attribute__((ext_vector_type(2)));
-        *reinterpret_cast<io2*>(o + 16 * VW * u + VW * j + e) =
-            io2{from_f32<IO>(attn_out(acc[u * VW + e][j], m, inv)), from_f32<IO>(attn_out(acc[u * VW + e + 1][j], m, inv))};
-      }
-  if (p.lse && go == 0) p.lse[row] = attn_lse(m, l);
   }
 }
 
 template <typename IO, typename KE>
 hipError_t launch_attn_t(const AttnParams& p, int d, dim3 grid, hipStream_t stream) {
   const bool uni = p.page_size % 16 == 0;
-  const int kind = p.ntile > 1 ? 2 : p.T > 1 ? 1 : 0;
+  const int kind = attn_kind(p.T, p.R);
 #define GDN_ATTN_LAUNCH(DD, UNI, KIND) \
   hipLaunchKernelGGL((attn_decode_kernel<IO, KE, DD, UNI, KIND>), grid, dim3(256), 0, stream, p)
-#define GDN_ATTN_CASE(DD)                                \
-  case DD:                                               \
-    if (uni && kind == 0) GDN_ATTN_LAUNCH(DD, true, 0);  \
-    else if (uni && kind == 1) GDN_ATTN_LAUNCH(DD, true, 1); \
-    else if (uni) GDN_ATTN_LAUNCH(DD, true, 2);          \
-    else if (kind == 0) GDN_ATTN_LAUNCH(DD, false, 0);   \
-    else if (kind == 1) GDN_ATTN_LAUNCH(DD, false, 1);   \
-    else GDN_ATTN_LAUNCH(DD, false, 2);                  \
+#define GDN_ATTN_KINDS(DD, UNI)                     \
+  if (kind == 0) GDN_ATTN_LAUNCH(DD, UNI, 0);       \
+  else if (kind == 1) GDN_ATTN_LAUNCH(DD, UNI, 1);  \
+  else if (kind == 2) GDN_ATTN_LAUNCH(DD, UNI, 2);  \
+  else GDN_ATTN_LAUNCH(DD, UNI, 3);
+#define GDN_ATTN_CASE(DD)          \
+  case DD:                         \
+    if (uni) {                     \
+      GDN_ATTN_KINDS(DD, true)     \
+    } else {                       \
+      GDN_ATTN_KINDS(DD, false)    \
+    }                              \
     break;
   switch (d) {
     GDN_ATTN_CASE(32)
@@ -698,6 +764,7 @@ hipError_t launch_attn_t(const AttnParams& p, int d, dim3 grid, hipStream_t stre
     default: return hipErrorInvalidValue;
   }
 #undef GDN_ATTN_CASE
+#undef GDN_ATTN_KINDS
 #undef GDN_ATTN_LAUNCH
   return hipGetLastError();
 }
