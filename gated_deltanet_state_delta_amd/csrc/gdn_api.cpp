@@ -366,6 +366,12 @@ gdn_status gdn_attn_decode(const gdn_attn_decode_args* p, void* stream) {
   if (a.q_stride_row < 0 || a.q_stride_token < 0 || a.q_stride_head < 0 || a.q_stride_row % unit != 0 ||
       a.q_stride_token % unit != 0 || a.q_stride_head % unit != 0)
     return fail(GDN_ERR_LAYOUT, "%s: q strides must be non-negative multiples of 16 bytes", f);
+  {
+    const uintptr_t q0 = (uintptr_t)a.q, o0 = (uintptr_t)a.out;
+    const uintptr_t q1 = q0 + ((size_t)(a.batch - 1) * a.q_stride_row + (size_t)(a.T - 1) * a.q_stride_token +
+                               (size_t)(a.hq - 1) * a.q_stride_head + a.d) * es;
+    if (q0 < o0 + (size_t)a.batch * a.T * a.hq * a.d * es && o0 < q1) return fail(GDN_ERR_LAYOUT, "%s: out overlaps q", f);
+  }
   if (a.n_pages > 0) {
     st = cache_layout(f, a.k_cache, a.k_stride_page, a.k_stride_token, a.k_stride_head, a.page_size, a.hkv, a.d, ce);
     if (st != GDN_OK) return st;

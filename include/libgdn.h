@@ -451,16 +451,16 @@ gdn_status gdn_conv1d(const gdn_conv1d_args* args, void* stream);
  *   q    [batch, T, hq, d] io_dtype, strides {row, token, head}
  *   out  [batch, T, hq, d] io_dtype, dense
  *   lse  [batch, T, hq] fp32 or NULL
- * 1 <= T <= 64, hq <= 65536; batch * hq * T below 2^31 and at most 2^23 groups
- * (row, key-value head, 16 of its T*hq/hkv query rows), GDN_ERR_UNSUPPORTED
- * above.  batch == 0 is a no-op.  Rows of the batch are independent:
+ * 1 <= T <= 64, hq <= 65536; batch * hq * T below 2^31, batch * max_pages *
+ * page_size below 2^37 and at most 2^23 groups (row, key-value head, 16 of its
+ * T*hq/hkv query rows), GDN_ERR_UNSUPPORTED above.  batch == 0 is a no-op.  Rows of the batch are independent:
  * tables may share pages.
  *
- * With a workspace of at least gdn_attn_decode_workspace_size(args) bytes
- * (device memory, 256-byte aligned; 0 when none is of use) the rows' lengths
- * are split over workgroups and joined by a second launch; with less, one
- * workgroup walks each row and key-value head: the same result up to rounding
- * order.  The size depends on sizes alone, not on lens.  The library keeps
+ * out must not overlap q.  With a workspace of at least
+ * gdn_attn_decode_workspace_size(args) bytes (device memory, 256-byte aligned;
+ * 0 when none is of use) the rows' keys are dealt evenly to the waves of one
+ * launch and the parts of a row joined by a second; with less, one wave walks
+ * each row and key-value head: the same result up to rounding order.  The size depends on sizes alone, not on lens.  The library keeps
  * nothing in the workspace between calls; calls that share one must not
  * overlap.
  * ------------------------------------------------------------------------- */

@@ -179,6 +179,73 @@ def test_split_rows(io, cache, page, d, hkv):
     assert ((one.double().cpu() - ref[0]).abs() <= bound).all()
 
 
+@pytest.mark.parametrize("page", [16, 9])
+@pytest.mark.parametrize("T,rows,hkv,most", [(1, 70, 64, 200), (3, 131, 32, 150), (1, 3, 64, 2500)])
+def test_shares_of_many_rows(T, rows, hkv, most, page):
+    """Many heads leave few shares: one ends a row, takes whole ones (empty
+    ones among them) and begins another, and long rows lie in several."""
+    r = torch.Generator().manual_seed(rows)
+    lens = torch.randint(0, most, (rows,), generator=r).to(torch.int32)
+    lens[rows // 2] = 0
+    table, n_pages = paged(lens, page, seed=rows)
+    kc, vc = caches(n_pages, page, hkv, 32, "f32", seed=rows)
+    q = torch.randn(rows, T, hkv, 32, generator=r)
+    _check(q, kc, vc, table, lens, "f32")
+
+
+@pytest.mark.parametrize("rows", [4096, 4097])
+def test_batches_of_thousands(rows):
+    """The largest batch that is dealt out in shares, and one more."""
+    r = torch.Generator().manual_seed(rows)
+    lens = torch.randint(0, 140, (rows,), generator=r).to(torch.int32)
+    lens[5] = 3000
+    table, n_pages = paged(lens, 16, seed=rows)
+    kc, vc = caches(n_pages, 16, 1, 32, "bf16", seed=1)
+    q = torch.randn(rows, 1, 2, 32, generator=r).bfloat16()
+    _check(q, kc, vc, table, lens, "bf16")
+
+
+def test_two_calls_at_once():
+    """Two streams, each call with a workspace of its own."""
+    lens = [3000, 900, 4000]
+    table, n_pages = paged(lens, 16)
+    kc, vc = (c.cuda() for c in caches(n_pages, 16, 4, 128, "bf16", seed=4))
+    table, n = table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    qs = [torch.randn(3, 1, 8, 128, generator=torch.Generator().manual_seed(i)).bfloat16().cuda() for i in range(2)]
+    want = [gdn.attn_decode(q, kc, vc, table, n) for q in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(20):
+        for i in range(2):
+            got[i].append(gdn.attn_decode(qs[i], kc, vc, table, n, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, want[i]) for x in got[i])
+
+
+def test_a_given_workspace_is_used_and_checked():
+    lens = torch.tensor([1500], dtype=torch.int32)
+    table, n_pages = paged(lens, 16)
+    kc, vc = (c.cuda() for c in caches(n_pages, 16, 2, 64, "bf16", seed=4))
+    q = torch.randn(1, 1, 4, 64, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    a = (q, kc, vc, table.cuda(), lens.cuda())
+    need = gdn.attn_decode_workspace_size(*a)
+    ws = torch.full((need + 256,), 255, dtype=torch.uint8).cuda()  # NaN where nothing is written
+    assert torch.equal(gdn.attn_decode(*a, workspace=ws), gdn.attn_decode(*a))
+    assert (ws[need:] == 255).all() and not (ws[:need] == 255).all()
+    with pytest.raises(ValueError):
+        gdn.attn_decode(*a, workspace=ws[:need - 4])
+
+
+def test_out_over_q_is_refused():
+    kc, vc = (c.cuda() for c in caches(4, 16, 2, 64, "bf16", seed=4))
+    q = torch.randn(1, 1, 4, 64).bfloat16().cuda()
+    with pytest.raises(gdn.GdnError):
+        gdn.attn_decode(q, kc, vc, torch.zeros(1, 2, dtype=torch.int32).cuda(), torch.ones(1, dtype=torch.int32).cuda(), out=q)
+
+
 def test_scores_far_apart_and_infinite():
     """Scores of +-10^4 (one key takes all the weight) and a key of -inf score."""
     lens = torch.tensor([300], dtype=torch.int32)

@@ -63,6 +63,8 @@ CACHE_ERRORS = [
     (dict(k_stride_head=32), 4), (dict(k_stride_token=64, k_stride_head=128), 4),  # overlapping rows
     (dict(v_stride_page=1024), 4), (dict(v_stride_page=2052), 4), (dict(k_stride_page=-2048), 4),
     (dict(workspace=FAKE + 16, workspace_bytes=1 << 30), 4),
+    (dict(out=FAKE), 4), (dict(out=FAKE + 1024), 4),                              # over q
+    (dict(batch=1 << 17, max_pages=1 << 26, page_table_stride=1 << 26), 5),       # positions of all rows
 ])
 def test_attn_decode_refuses(over, status):
     assert L.load().gdn_attn_decode(ctypes.byref(_attn(**over)), None) == status, L.load().gdn_last_error()
@@ -96,7 +98,7 @@ def test_workspace_depends_on_sizes_alone():
     one = f(ctypes.byref(_attn(batch=1, max_pages=1000, page_table_stride=1000)))
     assert one > 0 and one % 4 == 0
     assert f(ctypes.byref(_attn(batch=1, max_pages=1000, page_table_stride=1000, lens=None, q=None))) == one
-    assert f(ctypes.byref(_attn(batch=4096))) == 0  # enough rows without a split
+    assert f(ctypes.byref(_attn(batch=4096))) == 0  # tables of one step
     assert f(ctypes.byref(_attn(batch=1, max_pages=1))) == 0  # one short range
     assert f(None) == 0 and f(ctypes.byref(_attn(batch=0))) == 0
 
