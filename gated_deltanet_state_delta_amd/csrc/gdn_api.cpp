@@ -14,6 +14,7 @@
 
 #include "../../include/libgdn.h"
 #include "gdn_kernels.hpp"
+#include "gdn_paged.hpp"
 
 namespace {
 

@@ -38,7 +38,7 @@
 #pragma once
 
 #include "gdn_device.hpp"
-#include "gdn_kernels.hpp"
+#include "gdn_paged.hpp"
 
 namespace gdn {
 

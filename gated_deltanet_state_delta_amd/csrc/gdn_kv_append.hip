@@ -8,7 +8,7 @@
 // and page and leaves the two row offsets in LDS, then every thread copies
 // pieces of 8 elements (16-byte loads and stores for bf16).
 #include "gdn_device.hpp"
-#include "gdn_kernels.hpp"
+#include "gdn_paged.hpp"
 
 namespace gdn {
 

@@ -14,7 +14,7 @@
 // the tiles' numbers and the bits of the tiles that hold them.  No workgroup
 // waits for another inside a launch.
 #include "gdn_device.hpp"
-#include "gdn_kernels.hpp"
+#include "gdn_paged.hpp"
 
 namespace gdn {
 
