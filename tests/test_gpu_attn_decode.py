@@ -80,6 +80,21 @@ def test_new_tokens_and_groups(T, group, page):
     _check(q, kc, vc, table, lens, "bf16")
 
 
+@pytest.mark.parametrize("page", [16, 5])
+@pytest.mark.parametrize("T,group", [(1, 17), (4, 8), (3, 11), (8, 8), (16, 6), (40, 5)])
+@pytest.mark.parametrize("io,cache,d", [("bf16", "bf16", 128), ("bf16", "bf16", 256), ("f32", "f32", 256),
+                                        ("f32", "f32", 64), ("bf16", "e4m3", 256), ("f32", "e4m3", 128)])
+def test_row_tiles(io, cache, d, T, group, page):
+    """17 to 200 query rows of a key-value head: one to seven row tiles of one
+    or two times 16, alone in a workgroup's waves and several to a unit."""
+    lens = torch.tensor([T, 0, 30, 210], dtype=torch.int32)
+    table, n_pages = paged(lens, page, seed=T)
+    kc, vc = caches(n_pages, page, 2, d, cache, seed=T * 100 + group)
+    kc, vc = (poison_unheld(c, table, lens, page, float("nan")) for c in (kc, vc))
+    q = torch.randn(4, T, 2 * group, d, generator=torch.Generator().manual_seed(T)).to(DT[io])
+    _check(q, kc, vc, table, lens, io, *_scales(cache, 2))
+
+
 @pytest.mark.parametrize("page", [32, 6])
 @pytest.mark.parametrize("io,cache", [("bf16", "bf16"), ("f32", "f32"), ("f32", "e4m3")])
 def test_values_that_a_token_does_not_see(io, cache, page):
@@ -91,6 +106,7 @@ def test_values_that_a_token_does_not_see(io, cache, page):
     ks, vs = _scales(cache, 2)
     q = torch.randn(3, 4, 4, 64, generator=torch.Generator().manual_seed(3)).to(DT[io])
     clean = attn_ref(q, kc, vc, table, lens, 0.125, ks, vs)
+    wide = attn_ref(q.repeat_interleave(10, 2), kc, vc, table, lens, 0.125, ks, vs)  # 80 rows of a head
     kw, vw = kc.float(), vc.float()
     for b in range(3):
         j = int(lens[b]) - 1  # the newest token: seen by token 3 alone
@@ -98,11 +114,12 @@ def test_values_that_a_token_does_not_see(io, cache, page):
         vw[e, at] = float("nan") if cache == "e4m3" else float("inf")
         kw[e, at, 1] = float("nan")
     kc, vc = kw.to(kc.dtype), vw.to(vc.dtype)
-    out = gdn.attn_decode(q.cuda(), kc.cuda(), vc.cuda(), table.cuda(), lens.cuda(), k_scale=_dev(ks), v_scale=_dev(vs))
-    got = out.double().cpu()
-    bound = attn_bound(clean[0], clean[2], clean[3], lens, 64, io)
-    assert ((got - clean[0]).abs() <= bound)[:, :3].all()
-    assert not got[:, 3].isfinite().any()
+    for x, ref in ((q, clean), (q.repeat_interleave(10, 2), wide)):
+        out = gdn.attn_decode(x.cuda(), kc.cuda(), vc.cuda(), table.cuda(), lens.cuda(), k_scale=_dev(ks), v_scale=_dev(vs))
+        got = out.double().cpu()
+        bound = attn_bound(ref[0], ref[2], ref[3], lens, 64, io)
+        assert ((got - ref[0]).abs() <= bound)[:, :3].all()
+        assert not got[:, 3].isfinite().any()
 
 
 @pytest.mark.parametrize("page", [16, 3])
