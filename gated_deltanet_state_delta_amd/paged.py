@@ -31,21 +31,26 @@ def _on(stream, dev, tensors):
     """Where a call on tensors of `dev` runs: checks that all of them are there
     and returns the context that makes the device and stream current (None:
     they are), so that memory allocated for the call belongs to its stream."""
+    at = dev.index
     if dev.type != "cuda":
         raise ValueError("GPU tensors are required (libgdn has no CPU path)")
     for t in tensors:
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != at:
             raise ValueError("all tensors must be on one GPU (%s and %s)" % (dev, t.device))
     if stream is not None:
         if stream.device != dev:
             raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, dev))
         return torch.cuda.stream(stream)
-    return None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    return None if at == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
 def _checked(status):
     if status:
         _lib.check(status)
+
+
+def _library():
+    return _lib._lib or _lib.load()
 
 
 def _i32(t, name, shape, outside=None):
@@ -162,7 +167,7 @@ def attn_decode_args(q, k_cache, v_cache, page_table, lens, *, scale=None, k_sca
     table, table_stride, max_pages = _table(page_table, B)
     lens = _i32(lens, "lens", (B,))
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=q.device)
+        out = torch.empty_like(q) if q.is_contiguous() else torch.empty(shape, dtype=dtype, device=q.device)
     elif out.shape != shape or out.dtype is not dtype or not out.is_contiguous() or out.data_ptr() % 16:
         raise ValueError("out must be contiguous, 16-byte aligned, with q's shape and dtype")
     if lse is not None and (lse.shape != (B, T, hq) or lse.dtype != torch.float32 or not lse.is_contiguous()):
@@ -202,7 +207,7 @@ def attn_decode(q, k_cache, v_cache, page_table, lens, *, scale=None, k_scale=No
         with ctx:
             return attn_decode(q, k_cache, v_cache, page_table, lens, scale=scale, k_scale=k_scale, v_scale=v_scale,
                                out=out, return_lse=return_lse, workspace=workspace)
-    lib = _lib.load()
+    lib = _library()
     lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev) if return_lse else None
     a, keep, out = attn_decode_args(q, k_cache, v_cache, page_table, lens, scale=scale, k_scale=k_scale,
                                     v_scale=v_scale, out=out, lse=lse)
@@ -222,7 +227,15 @@ def attn_decode_workspace_size(q, k_cache, v_cache, page_table, lens, **kw) -> i
     """Bytes of device workspace that an attn_decode call with these arguments
     would use (gdn_attn_decode_workspace_size); the values of lens do not matter."""
     a, keep, _ = attn_decode_args(q, k_cache, v_cache, page_table, lens, **kw)
-    return int(_lib.load().gdn_attn_decode_workspace_size(byref(a)))
+    return int(_library().gdn_attn_decode_workspace_size(byref(a)))
+
+
+def _tokens(x, shape):
+    """[B, T, hkv, d] as rows of tokens one stride apart: x itself where it is
+    so laid out (the stride before the last two is then the tokens')."""
+    if x.is_contiguous():
+        return x
+    return x.reshape(shape[0] * shape[1], shape[2], shape[3])
 
 
 def kv_append_args(k, v, k_cache, v_cache, page_table, lens, *, cu_seqlens=None, k_scale=None, v_scale=None):
@@ -240,7 +253,7 @@ def kv_append_args(k, v, k_cache, v_cache, page_table, lens, *, cu_seqlens=None,
         if len(shape) != 4 or shape[0] != B:
             raise ValueError("k and v must be [B, T, hkv, d] ([tokens, hkv, d] with cu_seqlens)")
         total, hkv, d = B * shape[1], shape[2], shape[3]
-        k, v = k.reshape(total, hkv, d), v.reshape(total, hkv, d)
+        k, v = _tokens(k, shape), _tokens(v, shape)
     else:
         if len(shape) != 3:
             raise ValueError("with cu_seqlens k and v must be [tokens, hkv, d]")
@@ -253,7 +266,7 @@ def kv_append_args(k, v, k_cache, v_cache, page_table, lens, *, cu_seqlens=None,
     lens = _i32(lens, "lens", (B,))
     ks, vs = k.stride(), v.stride()
     a = _lib.KvAppendArgs(
-        total, B, hkv, d, _IO[dtype], cache_dtype, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+        total, B, hkv, d, _IO[dtype], cache_dtype, k.data_ptr(), ks[-3], ks[-2], v.data_ptr(), vs[-3], vs[-2],
         _ptr(cu_seqlens), k_cache.data_ptr(), *kcs, v_cache.data_ptr(), *vcs, cs[0], cs[1], max_pages,
         table.data_ptr(), table_stride, lens.data_ptr(), _ptr(k_scale), _ptr(v_scale))
     return a, (k, v, cu_seqlens, table, lens, k_scale, v_scale)
@@ -280,7 +293,7 @@ def kv_append(k, v, k_cache, v_cache, page_table, lens, *, cu_seqlens=None, k_sc
                              v_scale=v_scale)
     a, keep = kv_append_args(k, v, k_cache, v_cache, page_table, lens, cu_seqlens=cu_seqlens, k_scale=k_scale,
                              v_scale=v_scale)
-    _checked(_lib.load().gdn_kv_append(byref(a), _raw_stream(dev.index)))
+    _checked(_library().gdn_kv_append(byref(a), _raw_stream(dev.index)))
     del keep
     return k_cache, v_cache
 
@@ -321,7 +334,7 @@ def pages_copy(pool, src, dst, *, stream=None):
         raise ValueError("src must be [n]")
     n = src.shape[0]
     src, dst = _i32(src, "src", (n,), -1), _i32(dst, "dst", (n,), -1)
-    _checked(_lib.load().gdn_pages_copy(pool.data_ptr(), nbytes, stride, pool.shape[0], src.data_ptr(), dst.data_ptr(),
+    _checked(_library().gdn_pages_copy(pool.data_ptr(), nbytes, stride, pool.shape[0], src.data_ptr(), dst.data_ptr(),
                                         n, _raw_stream(dev.index)))
     return pool
 
@@ -361,7 +374,7 @@ def pages_args(page_table, lens, refs, page_size, out=None, apart=False, workspa
                 raise ValueError("out's %s overlaps the input" % name)
     ws, need = None, 0
     if workspace:
-        need = _lib.load().gdn_pages_workspace_size(rows, n)
+        need = _library().gdn_pages_workspace_size(rows, n)
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
     a = _lib.PagesArgs(rows, width, n, int(page_size), table.data_ptr(), table_stride, _ptr(lens_in), refs_in.data_ptr(),
                        to.data_ptr(), max(to.stride(0), width), _ptr(lens_to), refs_to.data_ptr(), _ptr(ws), need)
@@ -396,7 +409,7 @@ def pages_extend(page_table, lens, refs, add, page_size, *, out=None, stream=Non
     a, keep, (table, lens_to, refs_to) = pages_args(page_table, lens, refs, page_size, out)
     add = _i32(add, "add", (a.rows,))
     ok = torch.empty((a.rows,), dtype=torch.int32, device=dev)
-    _checked(_lib.load().gdn_pages_extend(byref(a), add.data_ptr(), ok.data_ptr(), _raw_stream(dev.index)))
+    _checked(_library().gdn_pages_extend(byref(a), add.data_ptr(), ok.data_ptr(), _raw_stream(dev.index)))
     del keep
     return table, lens_to, refs_to, ok
 
@@ -421,8 +434,8 @@ def pages_fork(page_table, lens, refs, parent, page_size, *, out=None, stream=No
             return pages_fork(page_table, lens, refs, parent, page_size, out=out)
     a, keep, (table, lens_to, refs_to) = pages_args(page_table, lens, refs, page_size, out, apart=True)
     parent = _i32(parent, "parent", (a.rows,), -1)
-    src, dst = (torch.empty((a.rows,), dtype=torch.int32, device=dev) for _ in range(2))
-    _checked(_lib.load().gdn_pages_fork(byref(a), parent.data_ptr(), src.data_ptr(), dst.data_ptr(),
+    src, dst = torch.empty((2, a.rows), dtype=torch.int32, device=dev)
+    _checked(_library().gdn_pages_fork(byref(a), parent.data_ptr(), src.data_ptr(), dst.data_ptr(),
                                         _raw_stream(dev.index)))
     del keep
     return table, lens_to, refs_to, src, dst
@@ -441,7 +454,7 @@ def pages_free(page_table, lens, refs, rows, page_size, *, out=None, stream=None
     if rows.shape != (a.rows,) or rows.dtype not in (torch.bool, torch.uint8):
         raise ValueError("rows must be bool or uint8 [%d]" % a.rows)
     rows = rows.contiguous()
-    _checked(_lib.load().gdn_pages_free(byref(a), rows.data_ptr(), _raw_stream(dev.index)))
+    _checked(_library().gdn_pages_free(byref(a), rows.data_ptr(), _raw_stream(dev.index)))
     del keep
     return to
 
@@ -463,7 +476,7 @@ def pages_compact(page_table, refs, *, out=None, stream=None):
     a, keep, (table, _, refs_to) = pages_args(page_table, None, refs, 1, out)
     src, dst = (torch.empty((a.n_pages // 2,), dtype=torch.int32, device=dev) for _ in range(2))
     n_live = torch.empty((1,), dtype=torch.int32, device=dev)
-    _checked(_lib.load().gdn_pages_compact(byref(a), src.data_ptr(), dst.data_ptr(), n_live.data_ptr(),
+    _checked(_library().gdn_pages_compact(byref(a), src.data_ptr(), dst.data_ptr(), n_live.data_ptr(),
                                            _raw_stream(dev.index)))
     del keep
     return table, refs_to, src, dst, n_live
