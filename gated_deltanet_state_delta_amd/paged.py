@@ -167,7 +167,7 @@ def attn_decode_args(q, k_cache, v_cache, page_table, lens, *, scale=None, k_sca
     table, table_stride, max_pages = _table(page_table, B)
     lens = _i32(lens, "lens", (B,))
     if out is None:
-        out = torch.empty_like(q) if q.is_contiguous() else torch.empty(shape, dtype=dtype, device=q.device)
+        out = torch.empty_like(q) if q.is_contiguous() else q.new_empty(shape)
     elif out.shape != shape or out.dtype is not dtype or not out.is_contiguous() or out.data_ptr() % 16:
         raise ValueError("out must be contiguous, 16-byte aligned, with q's shape and dtype")
     if lse is not None and (lse.shape != (B, T, hq) or lse.dtype != torch.float32 or not lse.is_contiguous()):
@@ -214,7 +214,7 @@ def attn_decode(q, k_cache, v_cache, page_table, lens, *, scale=None, k_scale=No
     need = lib.gdn_attn_decode_workspace_size(byref(a))
     if need > 0:
         if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = q.new_empty(need // q.element_size())  # (a multiple of 4 bytes)
         elif workspace.numel() * workspace.element_size() < need or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous buffer of at least %d bytes" % need)
         a.workspace, a.workspace_bytes = workspace.data_ptr(), need
@@ -355,9 +355,9 @@ def pages_args(page_table, lens, refs, page_size, out=None, apart=False, workspa
     lens_in = None if lens is None else _i32(lens, "lens", (rows,))
     dev = page_table.device
     if out is None:
-        to = torch.empty((rows, width), dtype=torch.int32, device=dev)
-        lens_to = None if lens is None else torch.empty((rows,), dtype=torch.int32, device=dev)
-        refs_to = torch.empty((n,), dtype=torch.int32, device=dev)
+        to = torch.empty_like(table) if table.is_contiguous() else table.new_empty(rows, width)
+        lens_to = None if lens is None else torch.empty_like(lens_in)
+        refs_to = torch.empty_like(refs_in)
     else:
         to, refs_to = out[0], out[-1]
         lens_to = None if lens is None else out[1]
@@ -375,7 +375,7 @@ def pages_args(page_table, lens, refs, page_size, out=None, apart=False, workspa
     ws, need = None, 0
     if workspace:
         need = _library().gdn_pages_workspace_size(rows, n)
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws = refs_in.new_empty(need // 4)
     a = _lib.PagesArgs(rows, width, n, int(page_size), table.data_ptr(), table_stride, _ptr(lens_in), refs_in.data_ptr(),
                        to.data_ptr(), max(to.stride(0), width), _ptr(lens_to), refs_to.data_ptr(), _ptr(ws), need)
     return a, (table, lens_in, refs_in, ws), (to, lens_to, refs_to)
@@ -408,7 +408,7 @@ def pages_extend(page_table, lens, refs, add, page_size, *, out=None, stream=Non
             return pages_extend(page_table, lens, refs, add, page_size, out=out)
     a, keep, (table, lens_to, refs_to) = pages_args(page_table, lens, refs, page_size, out)
     add = _i32(add, "add", (a.rows,))
-    ok = torch.empty((a.rows,), dtype=torch.int32, device=dev)
+    ok = torch.empty_like(add)
     _checked(_library().gdn_pages_extend(byref(a), add.data_ptr(), ok.data_ptr(), _raw_stream(dev.index)))
     del keep
     return table, lens_to, refs_to, ok
@@ -434,7 +434,7 @@ def pages_fork(page_table, lens, refs, parent, page_size, *, out=None, stream=No
             return pages_fork(page_table, lens, refs, parent, page_size, out=out)
     a, keep, (table, lens_to, refs_to) = pages_args(page_table, lens, refs, page_size, out, apart=True)
     parent = _i32(parent, "parent", (a.rows,), -1)
-    src, dst = torch.empty((2, a.rows), dtype=torch.int32, device=dev)
+    src, dst = torch.empty_like(parent), torch.empty_like(parent)
     _checked(_library().gdn_pages_fork(byref(a), parent.data_ptr(), src.data_ptr(), dst.data_ptr(),
                                         _raw_stream(dev.index)))
     del keep
@@ -474,8 +474,8 @@ def pages_compact(page_table, refs, *, out=None, stream=None):
         with ctx:
             return pages_compact(page_table, refs, out=out)
     a, keep, (table, _, refs_to) = pages_args(page_table, None, refs, 1, out)
-    src, dst = (torch.empty((a.n_pages // 2,), dtype=torch.int32, device=dev) for _ in range(2))
-    n_live = torch.empty((1,), dtype=torch.int32, device=dev)
+    src = refs_to.new_empty(a.n_pages // 2)
+    dst, n_live = torch.empty_like(src), refs_to.new_empty(1)
     _checked(_library().gdn_pages_compact(byref(a), src.data_ptr(), dst.data_ptr(), n_live.data_ptr(),
                                            _raw_stream(dev.index)))
     del keep
