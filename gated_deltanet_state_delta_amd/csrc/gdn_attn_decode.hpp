@@ -244,6 +244,12 @@ constexpr int attn_rows16(int kind, int d, int io) { return kind < 2 || (io == 4
 // registers from heads of 128 on.
 constexpr int attn_waves(int es, int d, int kind) { return kind > 1 ? d > 64 ? 1 : 2 : attn_occ(es, d); }
 
+// Keys of a wave's tile, a multiple of the products' depth.
+constexpr int attn_tile(int es, int d) {
+  const int keys = 8192 / attn_occ(es, d) / (d * es);
+  return keys > 64 ? 64 : keys < 16 ? 16 : keys;
+}
+
 template <typename IO, typename KE, int D, int KIND>
 struct AttnCfg {
   static constexpr int ES = sizeof(KE);
@@ -252,9 +258,7 @@ struct AttnCfg {
   static constexpr int kmin(int a, int b) { return a < b ? a : b; }
   static constexpr int KW = kmin(16 / ES, D / 4), NC = D / (4 * KW);    // elements per K piece, pieces per row and lane
   static constexpr int VW = kmin(16 / ES, D / 16), U = D / (16 * VW);   // the same for V
-  // Keys of a tile, a multiple of the products' depth.
-  static constexpr int OCC = attn_waves(ES, D, KIND), KTW = 8192 / attn_occ(ES, D) / (D * ES);
-  static constexpr int KT = KTW > 64 ? 64 : KTW < 16 ? 16 : KTW;
+  static constexpr int OCC = attn_waves(ES, D, KIND), KT = attn_tile(ES, D);
   static constexpr int NT = KT / 16;
   static constexpr int NA = D / 16;  // accumulator tiles
 };
