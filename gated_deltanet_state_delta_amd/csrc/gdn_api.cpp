@@ -357,8 +357,9 @@ gdn_status gdn_attn_decode(const gdn_attn_decode_args* p, void* stream) {
   // one workgroup per row, key-value head and 16 query rows; a grid has at most 2^24 of 256 threads
   if ((int64_t)a.batch * a.hkv * (((int64_t)a.T * (a.hq / a.hkv) + 15) / 16) > (int64_t(1) << 23))
     return fail(GDN_ERR_UNSUPPORTED, "%s: batch * hkv * ceil(T * hq / hkv / 16) must be at most 2^23", f);
-  if ((int64_t)a.batch * (((int64_t)a.max_pages * a.page_size + 63) / 64) >= (int64_t(1) << 31))
-    return fail(GDN_ERR_UNSUPPORTED, "%s: batch * max_pages * page_size must be below 2^37", f);
+  // the rows' tiles of 16 keys and more are counted in 32 bits
+  if ((int64_t)a.batch * (((int64_t)a.max_pages * a.page_size + 15) / 16 + 1) >= (int64_t(1) << 31))
+    return fail(GDN_ERR_UNSUPPORTED, "%s: batch * (max_pages * page_size / 16 + 1) must be below 2^31", f);
   if (!a.q || !a.out || !a.lens || (a.max_pages > 0 && !a.page_table) || (a.n_pages > 0 && (!a.k_cache || !a.v_cache)))
     return fail(GDN_ERR_NULL, "%s: q, caches, page_table, lens and out are required", f);
   const size_t es = elem_size(a.io_dtype), ce = a.cache_dtype == GDN_E4M3 ? 1 : es;

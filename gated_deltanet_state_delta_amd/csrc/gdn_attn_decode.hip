@@ -110,9 +110,9 @@ static int attn_tiles(const gdn_attn_decode_args& a) {
   return (R + rows - 1) / rows;
 }
 static int attn_shares(const gdn_attn_decode_args& a) {
-  const int64_t cap = (int64_t)a.max_pages * a.page_size, steps = a.batch * ((cap + kStep - 1) / kStep);
-  const int es = a.cache_dtype == GDN_E4M3 ? 1 : a.io_dtype == GDN_BF16 ? 2 : 4;
-  const int alone = attn_tile(es, a.d) < 32 ? kStep : 128;
+  const int es = a.cache_dtype == GDN_E4M3 ? 1 : a.io_dtype == GDN_BF16 ? 2 : 4, tile = attn_tile(es, a.d);
+  const int64_t cap = (int64_t)a.max_pages * a.page_size, steps = a.batch * ((cap + tile - 1) / tile);
+  const int alone = tile < 32 ? 64 : 128;
   if (cap <= alone || a.batch > kMostRows || (int64_t)a.batch * a.hq * a.T > (1 << 24)) return 0;
   const int64_t each = (int64_t)a.hkv * attn_tiles(a);  // waves of a share
   const int64_t fill = 1024 * attn_waves(es, a.d, attn_kind(a.T, a.T * (a.hq / a.hkv))) / each;

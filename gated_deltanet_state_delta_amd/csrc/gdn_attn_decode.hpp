@@ -14,7 +14,7 @@
 // Work split: a wave walks keys of one key-value head for 16 query rows, by
 // itself: no barrier, and no LDS where pages are whole subtiles.  The lengths
 // are known on the device only, so the keys of all rows, laid end to end in
-// steps of 64, are dealt out evenly: each of a fixed number of waves (as many
+// steps of one tile, are dealt out evenly: each of a fixed number of waves (as many
 // as the card holds at once) finds its share from the lengths and may end one
 // row, take some whole ones and begin another.  Whole rows are finished on
 // the spot; the parts of a row that several waves share go to the workspace
@@ -70,10 +70,10 @@ __device__ __forceinline__ int attn_len(const AttnParams& p, int b) {
   return p.n_pages == 0 ? 0 : min(max(len, 0), p.cap);
 }
 
-constexpr int kStep = 64;  // keys; every share is whole steps of a row
-
-// A row's steps; an empty row has one, which writes its zeros.
-__device__ __forceinline__ int attn_steps(int len) { return max(1, (len + kStep - 1) / kStep); }
+// A row's steps of STEP keys (one tile; every share is whole steps of a row);
+// an empty row has one, which writes its zeros.
+template <int STEP>
+__device__ __forceinline__ int attn_steps(int len) { return max(1, (len + STEP - 1) / STEP); }
 
 __device__ __forceinline__ int wave_scan_add_i(int v) {  // inclusive, in lane order
   v += dpp_i<0x111, 0xF>(0, v);
@@ -93,17 +93,18 @@ struct AttnShare { int b, at, n, size; };
 // sums the steps of batch / 64 neighbouring rows; every wave finds the share
 // for itself, without LDS.  All steps together are below 2^31 (checked on the
 // host against the tables' sizes).
+template <int STEP>
 __device__ __forceinline__ AttnShare attn_share(const AttnParams& p, int k, int lane) {
   AttnShare r;
   if (!p.plan) {
     r.b = k;
     r.at = 0;
-    r.n = r.size = k < p.batch ? attn_steps(attn_len(p, k)) : 0;
+    r.n = r.size = k < p.batch ? attn_steps<STEP>(attn_len(p, k)) : 0;
     return r;
   }
   const int per = (p.batch + 63) >> 6, i0 = lane * per, i1 = min(p.batch, i0 + per);
   int mine = 0;
-  for (int i = i0; i < i1; ++i) mine += attn_steps(attn_len(p, i));
+  for (int i = i0; i < i1; ++i) mine += attn_steps<STEP>(attn_len(p, i));
   const int upto = wave_scan_add_i(mine), from = upto - mine;
   const int all = __builtin_amdgcn_readlane(upto, 63);
   r.size = (int)(((int64_t)all + p.shares - 1) / p.shares);
@@ -115,7 +116,7 @@ __device__ __forceinline__ AttnShare attn_share(const AttnParams& p, int k, int 
   int b = i0, at = (int)first - from;
   if (here)
     for (;; ++b) {
-      const int n = attn_steps(attn_len(p, b));
+      const int n = attn_steps<STEP>(attn_len(p, b));
       if (at < n) break;
       at -= n;
     }
@@ -290,14 +291,14 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND>::OCC)) attn_dec
   const int rt = (int)(blockIdx.x / 8 % nwg) * rtw + wave % rtw;
   const int h = unit % p.hkv, share_id = unit / p.hkv;
   if (share_id >= p.shares || rt >= p.ntile) return;
-  AttnShare share = attn_share(p, share_id, lane);
+  AttnShare share = attn_share<KT>(p, share_id, lane);
 
   const float s_scale = p.scale_log2 * (p.k_scale ? p.k_scale[h] : 1.0f);
 
   while (share.n > 0) {
-  const int b = share.b, len = attn_len(p, b), row_steps = attn_steps(len), at = share.at;
+  const int b = share.b, len = attn_len(p, b), row_steps = attn_steps<KT>(len), at = share.at;
   const int take = min(share.n, row_steps - at);
-  const int c0 = at * kStep, c1 = min(len, (at + take) * kStep);
+  const int c0 = at * KT, c1 = min(len, (at + take) * KT);
   const bool whole = take == row_steps;
   const int slot = 2 * share_id + (at == 0);  // of a part: one that begins a row, one that does not
   if (p.plan && at == 0 && h == 0 && rt == 0 && lane == 0)
@@ -371,8 +372,6 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND>::OCC)) attn_dec
   Raw<KW * ES> kr[NT][NC];
   Raw<VW * ES> vr[NT][4][U];
 
-  const int first = c0;
-  constexpr int STEP = KT;
 
   // ---- page lookups
   auto page_of = [&](int key) -> int { return (int)(((uint64_t)(uint32_t)key * p.page_mul) >> p.page_shift); };
@@ -452,18 +451,18 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND>::OCC)) attn_dec
   Ents ent_cur = {}, ent_next = {};
   int ent1_next = 0;
   int par = 0;
-  if (first < c1) {
+  if (c0 < c1) {
     if constexpr (UNI) {
-      ent_cur = load_ents(first);
-      issue_k_uni(ent_cur, first);
-      ent_next = load_ents(first + STEP);
+      ent_cur = load_ents(c0);
+      issue_k_uni(ent_cur, c0);
+      ent_next = load_ents(c0 + KT);
     } else {
-      publish(load_ent1(first), first, 0);
+      publish(load_ent1(c0), c0, 0);
       issue_k_any(0);
-      ent1_next = load_ent1(first + STEP);
+      ent1_next = load_ent1(c0 + KT);
     }
   }
-  for (int key0 = first; key0 < c1; key0 += STEP) {
+  for (int key0 = c0; key0 < c1; key0 += KT) {
     if constexpr (UNI) issue_v_uni(ent_cur, key0);
     else issue_v_any(par);
 
@@ -507,15 +506,15 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND>::OCC)) attn_dec
 #pragma unroll
       for (int n = 0; n < NT; ++n)
         if (ent_cur.e[n] < 0 || ent_cur.e[n] >= p.n_pages) sub_ok &= ~(1u << n);
-      if (key0 + STEP < c1) issue_k_uni(ent_next, key0 + STEP);
+      if (key0 + KT < c1) issue_k_uni(ent_next, key0 + KT);
       ent_cur = ent_next;
-      ent_next = load_ents(key0 + 2 * STEP);
+      ent_next = load_ents(key0 + 2 * KT);
     } else {
       par ^= 1;
-      if (key0 + STEP < c1) {
-        publish(ent1_next, key0 + STEP, par);
+      if (key0 + KT < c1) {
+        publish(ent1_next, key0 + KT, par);
         issue_k_any(par);
-        ent1_next = load_ent1(key0 + 2 * STEP);
+        ent1_next = load_ent1(key0 + 2 * KT);
       }
     }
 

@@ -451,10 +451,10 @@ gdn_status gdn_conv1d(const gdn_conv1d_args* args, void* stream);
  *   q    [batch, T, hq, d] io_dtype, strides {row, token, head}
  *   out  [batch, T, hq, d] io_dtype, dense
  *   lse  [batch, T, hq] fp32 or NULL
- * 1 <= T <= 64, hq <= 65536; batch * hq * T below 2^31, batch * max_pages *
- * page_size below 2^37 and at most 2^23 groups (row, key-value head, 16 of its
- * T*hq/hkv query rows), GDN_ERR_UNSUPPORTED above.  batch == 0 is a no-op.  Rows of the batch are independent:
- * tables may share pages.
+ * 1 <= T <= 64, hq <= 65536; batch * hq * T below 2^31, batch * (max_pages *
+ * page_size / 16 + 1) below 2^31 and at most 2^23 groups (row, key-value head,
+ * 16 of its T*hq/hkv query rows), GDN_ERR_UNSUPPORTED above.  batch == 0 is a
+ * no-op.  Rows of the batch are independent: tables may share pages.
  *
  * out must not overlap q.  With a workspace of at least
  * gdn_attn_decode_workspace_size(args) bytes (device memory, 256-byte aligned;
