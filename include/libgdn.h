@@ -430,9 +430,9 @@ gdn_status gdn_conv1d(const gdn_conv1d_args* args, void* stream);
  * Common requirements: max_pages * page_size at most 2^30; d in {32, 64, 128,
  * 256}; hq a multiple of hkv (query head h reads key-value head h*hkv/hq);
  * a cache has io_dtype's type or GDN_E4M3; caches, q, k, v and out 16-byte
- * aligned, their strides multiples of 16 bytes, not smaller than the dense
- * extents of what they step over (a cache's token and head strides each at
- * least d) and, for token and head strides, below 2^23 elements.
+ * aligned, their strides non-negative multiples of 16 bytes; a cache's token
+ * and head strides in [d, 2^23) elements, its rows apart and its page stride
+ * not smaller than a page.
  * ========================================================================= */
 
 /* ----------------------------------------------------------------------------
@@ -460,9 +460,9 @@ gdn_status gdn_conv1d(const gdn_conv1d_args* args, void* stream);
  * gdn_attn_decode_workspace_size(args) bytes (device memory, 256-byte aligned;
  * 0 when none is of use) the rows' keys are dealt evenly to the waves of one
  * launch and the parts of a row joined by a second; with less, one wave walks
- * each row and key-value head: the same result up to rounding order.  The size depends on sizes alone, not on lens.  The library keeps
- * nothing in the workspace between calls; calls that share one must not
- * overlap.
+ * each row and key-value head: the same result up to rounding order.  The size
+ * depends on sizes alone, not on lens.  The library keeps nothing in the
+ * workspace between calls; calls that share one must not overlap.
  * ------------------------------------------------------------------------- */
 typedef struct {
   int32_t batch, T, hq, hkv, d;
