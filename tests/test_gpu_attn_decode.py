@@ -173,6 +173,22 @@ def test_layouts(layout, page):
     assert ((out.double().cpu() - want[0]).abs() <= attn_bound(want[0], want[2], want[3], lens, 64, "bf16")).all()
 
 
+@pytest.mark.parametrize("n_pages,page,hkv,heads_first", [(1, 64, 2, False), (1, 64, 1, True), (40, 1, 3, True),
+                                                          (40, 1, 1, False), (5, 16, 1, True), (1, 1, 1, False)])
+def test_dimensions_of_one_entry(n_pages, page, hkv, heads_first):
+    """Strides of dimensions of one entry mean nothing."""
+    n = n_pages * page - n_pages * page // 5
+    lens = torch.tensor([n, max(n - 3, 0)], dtype=torch.int32)
+    table = torch.randperm(n_pages, generator=torch.Generator().manual_seed(1)).to(torch.int32).repeat(2, 1)
+    kc, vc = caches(n_pages, page, hkv, 64, "bf16", seed=3, heads_first=heads_first)
+    q = torch.randn(2, 1, 2 * hkv, 64, generator=torch.Generator().manual_seed(1)).bfloat16()
+    want = attn_ref(q, kc, vc, table, lens, 0.125)
+    odd = lambda c: torch.as_strided(c, c.shape, [7 if sz == 1 else st for sz, st in zip(c.shape[:3], c.stride())] + [1])
+    for k, v in ((_dev(kc), _dev(vc)), (odd(_dev(kc)), odd(_dev(vc)))):
+        out = gdn.attn_decode(q.cuda(), k, v, table.cuda(), lens.cuda())
+        assert ((out.double().cpu() - want[0]).abs() <= attn_bound(want[0], want[2], want[3], lens, 64, "bf16")).all()
+
+
 @pytest.mark.parametrize("page,d,hkv", [(16, 128, 1), (64, 64, 2), (5, 128, 1), (1, 256, 1)])
 @pytest.mark.parametrize("io,cache", [("bf16", "bf16"), ("f32", "f32"), ("bf16", "e4m3")])
 def test_split_rows(io, cache, page, d, hkv):

@@ -130,6 +130,24 @@ def test_offsets_clamped_and_strided_input():
         assert torch.equal(a.float().cpu(), b)
 
 
+def test_parts_of_a_projection_and_a_given_stream():
+    """[B, T, hkv, d] slices of one projection, on a stream of their own."""
+    table, n_pages = paged([9, 20], 8)
+    kc, vc = caches(n_pages, 8, 2, 64, "f32", 3)
+    qkv = torch.randn(2, 3, 8, 64, generator=torch.Generator().manual_seed(1))
+    lens = torch.tensor([9, 20], dtype=torch.int32)
+    want = [_want(c, qkv[:, :, i:i + 2].reshape(6, 2, 64), [3, 3], table, lens, 8, None) for c, i in ((kc, 4), (vc, 6))]
+    dq, k, v, t, n = (x.cuda() for x in (qkv, kc, vc, table, lens))
+    free = min(set(range(n_pages)) - set(table.flatten().tolist()))
+    want[0][free] = want[0][int(table[0, 0])]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    gdn.kv_append(dq[:, :, 4:6], dq[:, :, 6:8], k, v, t, n, stream=side)
+    gdn.pages_copy(k, t[0, :1], torch.tensor([free], dtype=torch.int32).cuda(), stream=side)
+    side.synchronize()
+    assert torch.equal(k.cpu(), want[0]) and torch.equal(v.cpu(), want[1])
+
+
 def test_nothing_to_write():
     kc, vc = (c.cuda() for c in caches(2, 16, 2, 64, "bf16", 3))
     before = kc.clone()

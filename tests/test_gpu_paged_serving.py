@@ -94,3 +94,43 @@ def test_a_batch_lives_through_prompts_forks_and_compaction(page, cache):
             attend(1)
     table, lens, refs = gdn.pages_free(table, lens, refs, torch.ones(rows, dtype=torch.bool).cuda(), page)
     assert int(refs.abs().sum()) == 0 and int(lens.sum()) == 0
+
+
+def test_a_decode_step_captured_once_and_replayed():
+    """Grow, append and attend in one graph, in place: every replay is one more
+    token of each row, checked against the rows' histories."""
+    rows, width, page, hkv, hq, d, n_pages = 4, 8, 16, 2, 8, 128, 40
+    gen = torch.Generator().manual_seed(1)
+    draw = lambda *s: torch.randn(*s, generator=gen).bfloat16()
+    kc, vc = (torch.zeros(n_pages, page, hkv, d, dtype=torch.bfloat16).cuda() for _ in range(2))
+    table = torch.full((rows, width), -1, dtype=torch.int32).cuda()
+    lens, refs = torch.zeros(rows, dtype=torch.int32).cuda(), torch.zeros(n_pages, dtype=torch.int32).cuda()
+    one = torch.ones(rows, dtype=torch.int32).cuda()
+    start = [14, 0, 31, 60]
+    _, _, _, ok = gdn.pages_extend(table, lens, refs, torch.tensor(start, dtype=torch.int32).cuda(), page, out=(table, lens, refs))
+    k, v = draw(sum(start), hkv, d), draw(sum(start), hkv, d)
+    cu = [sum(start[:i]) for i in range(rows + 1)]
+    gdn.kv_append(k.cuda(), v.cuda(), kc, vc, table, lens, cu_seqlens=torch.tensor(cu, dtype=torch.int32).cuda())
+    hist = [(k[cu[b]:cu[b + 1]], v[cu[b]:cu[b + 1]]) for b in range(rows)]
+    q1, k1, v1 = (torch.zeros(rows, 1, h, d, dtype=torch.bfloat16).cuda() for h in (hq, hkv, hkv))
+    gdn.attn_decode(q1, kc, vc, table, lens)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gdn.pages_extend(table, lens, refs, one, page, out=(table, lens, refs))
+        gdn.kv_append(k1, v1, kc, vc, table, lens)
+        out = gdn.attn_decode(q1, kc, vc, table, lens)
+    for step in range(6):
+        q, k, v = draw(rows, 1, hq, d), draw(rows, 1, hkv, d), draw(rows, 1, hkv, d)
+        q1.copy_(q), k1.copy_(k), v1.copy_(v)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.double().cpu()
+        assert torch.equal(gdn.attn_decode(q1, kc, vc, table, lens), out)  # eager work between the replays
+        for b in range(rows):
+            hist[b] = tuple(torch.cat([h, x[b]]) for h, x in zip(hist[b], (k, v)))
+            ln = torch.tensor([start[b] + step + 1])
+            want, _, mean, size = attn_ref(q[b:b + 1], hist[b][0][None], hist[b][1][None], torch.zeros(1, 1, dtype=torch.int32),
+                                           ln, d ** -0.5)
+            assert ((got[b:b + 1] - want).abs() <= attn_bound(want, mean, size, ln, d, "bf16")).all(), (step, b)
+    assert lens.tolist() == [s + 6 for s in start] and int(refs.sum()) == sum(-(-(s + 6) // page) for s in start)
