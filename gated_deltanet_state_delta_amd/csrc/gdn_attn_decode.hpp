@@ -14,12 +14,11 @@
 // Work split: a wave walks keys of one key-value head for 16 query rows, by
 // itself: no barrier, and no LDS where pages are whole subtiles.  The lengths
 // are known on the device only, so the keys of all rows, laid end to end in
-// steps of one tile, are dealt out evenly: each of a fixed number of waves (as many
-// as the card holds at once) finds its share from the lengths and may end one
-// row, take some whole ones and begin another.  Whole rows are finished on
-// the spot; the parts of a row that several waves share go to the workspace
-// as (m, l, unnormalised output) and attn_join_kernel joins them in a fixed
-// order.
+// steps of one tile, are dealt out evenly: each of a fixed number of waves (as
+// many as the card holds at once) finds its share from the lengths and may end
+// one row, take some whole ones and begin another.  Whole rows are finished on
+// the spot; the parts of a row that several waves share go to the workspace as
+// (m, l, unnormalised output) and attn_join_kernel joins them in a fixed order.
 //
 // No LDS and no shuffles between the cache and MFMA.  Both products are
 // taken transposed, so every operand is in the form in which a lane loads
@@ -231,7 +230,8 @@ constexpr int attn_occ(int es, int d) { return es > 1 && d >= 128 ? 1 : 2; }
 // IO: type of q and out; KE: cache element.  The products are bf16, or fp32
 // for an fp32 cache.  fp32 queries and weights over an e4m3 cache, whose values
 // bf16 holds exactly, enter as three bf16 terms (24 bits): 3 products of 16x16x32
-// instead of 8 of 16x16x4, which are 16 times slower each.
+// instead of 8 of 16x16x4 at twice the cycles each (64 ragged rows up to 8192 tokens,
+// 8 heads of 128: 105 us against 186).
 //
 // KIND 0: one new token, up to 16 query rows of a key-value head.  1: several
 // new tokens, up to 16 rows.  2: up to 32 rows.  3: more.
@@ -273,19 +273,20 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND>::OCC)) attn_dec
   typedef AttnCfg<IO, KE, D, KIND> C;
   constexpr int KT = C::KT, NT = C::NT, NC = C::NC, KW = C::KW, VW = C::VW, U = C::U, NA = C::NA, ES = C::ES;
   constexpr int QT = C::QT, PT = C::PT, RT = attn_rows16(KIND, D, sizeof(IO));
-  // Where no second wave reads a key, non-temporal loads leave the caches alone
-  // (the batch above, at two waves of 8 KiB: 184 us against 201 with ordinary ones; 64
-  // rows that share all of their 4096 tokens 94 against 85).
+  // Where no second wave reads a key, non-temporal loads leave the caches
+  // alone (the bf16 batch above, at two waves of 8 KiB: 184 us against 201 with
+  // ordinary ones; 64 rows that share all of their 4096 tokens 94 against 85).
   constexpr bool BF = C::BF, MT = KIND > 0, ONCE = KIND < 2 || (KIND == 2 && RT == 2);
   constexpr uint64_t kNone = ~0ull;
   __shared__ uint64_t offs[UNI ? 1 : 4][2][2][UNI ? 1 : KT];  // [wave][parity][K, V][key]
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // Wave -> (share, head, row tile of 16 RT rows).  A workgroup's waves take the row tiles
-  // of one (share, head), which read the same keys, or neighbouring heads,
-  // whose rows are neighbours in a tokens-first cache; further workgroups of
-  // one (share, head) are 8 apart and so on one XCD (they go round the 8).
+  // Wave -> (share, head, row tile of 16 RT rows).  A workgroup's waves take
+  // the row tiles of one (share, head), which read the same keys, or
+  // neighbouring heads, whose rows are neighbours in a tokens-first cache;
+  // further workgroups of one (share, head) are 8 apart and so on one XCD
+  // (workgroups go round the 8).
   const int rtw = p.ntile > 2 ? 4 : p.ntile, nwg = (p.ntile + rtw - 1) / rtw;
   const int unit = (int)((blockIdx.x / (8 * nwg) * 8 + (blockIdx.x & 7)) * (4 / rtw)) + wave / rtw;
   const int rt = (int)(blockIdx.x / 8 % nwg) * rtw + wave % rtw;
@@ -296,448 +297,450 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND>::OCC)) attn_dec
   const float s_scale = p.scale_log2 * (p.k_scale ? p.k_scale[h] : 1.0f);
 
   while (share.n > 0) {
-  const int b = share.b, len = attn_len(p, b), row_steps = attn_steps<KT>(len), at = share.at;
-  const int take = min(share.n, row_steps - at);
-  const int c0 = at * KT, c1 = min(len, (at + take) * KT);
-  const bool whole = take == row_steps;
-  const int slot = 2 * share_id + (at == 0);  // of a part: one that begins a row, one that does not
-  if (p.plan && at == 0 && h == 0 && rt == 0 && lane == 0)
-    p.plan[b] = make_int2(share_id, 1 + (row_steps - take + share.size - 1) / share.size);
-  share.n -= take;
-  share.b = b + 1;
-  share.at = 0;
+    const int b = share.b, len = attn_len(p, b), row_steps = attn_steps<KT>(len), at = share.at;
+    const int take = min(share.n, row_steps - at);
+    const int c0 = at * KT, c1 = min(len, (at + take) * KT);
+    const bool whole = take == row_steps;
+    const int slot = 2 * share_id + (at == 0);  // of a part: one that begins a row, one that does not
+    if (p.plan && at == 0 && h == 0 && rt == 0 && lane == 0)
+      p.plan[b] = make_int2(share_id, 1 + (row_steps - take + share.size - 1) / share.size);
+    share.n -= take;
+    share.b = b + 1;
+    share.at = 0;
 
-  // The lane's place, opaque to the compiler: what follows from it is computed
-  // for each row anew rather than held in registers across the walk.
-  int own = lane;
-  asm volatile("" : "+v"(own));
-  const int x = own & 15, g = own >> 4;
-  // This lane's query rows, one of each 16: row r is token r / group, query
-  // head h*group + r % group, and sees keys below lim.
-  int lim[RT], t_row[RT];
-  bf8 qb[RT][BF ? QT : 1][BF ? D / 32 : 1];
-  float qf[RT][BF ? 1 : D / 4];
+    // The lane's place, opaque to the compiler: what follows from it is computed
+    // for each row anew rather than held in registers across the walk.
+    int own = lane;
+    asm volatile("" : "+v"(own));
+    const int x = own & 15, g = own >> 4;
+    // This lane's query rows, one of each 16: row r is token r / group, query
+    // head h*group + r % group, and sees keys below lim.
+    int lim[RT], t_row[RT];
+    bf8 qb[RT][BF ? QT : 1][BF ? D / 32 : 1];
+    float qf[RT][BF ? 1 : D / 4];
 #pragma unroll
-  for (int q = 0; q < RT; ++q) {
-    const int r = (rt * RT + q) * 16 + x;
-    const bool row_ok = r < p.R;
-    t_row[q] = row_ok ? r / p.group : 0;
-    const int hq_row = h * p.group + (row_ok ? r % p.group : 0);
-    lim[q] = row_ok ? max(0, min(len, len - p.T + t_row[q] + 1)) : 0;
-    const char* qp = (const char*)p.q + b * p.q_sb + t_row[q] * p.q_st + hq_row * p.q_sh;
+    for (int q = 0; q < RT; ++q) {
+      const int r = (rt * RT + q) * 16 + x;
+      const bool row_ok = r < p.R;
+      t_row[q] = row_ok ? r / p.group : 0;
+      const int hq_row = h * p.group + (row_ok ? r % p.group : 0);
+      lim[q] = row_ok ? max(0, min(len, len - p.T + t_row[q] + 1)) : 0;
+      const char* qp = (const char*)p.q + b * p.q_sb + t_row[q] * p.q_st + hq_row * p.q_sh;
 #pragma unroll
-    for (int i = 0; i < D / 4; i += BF ? 8 : 4) {
-      const int c = i / KW, d = 4 * KW * c + KW * g + i % KW;
-      if constexpr (BF && sizeof(IO) == 2) {
-        bf8 t = {};
-        if (row_ok) t = *reinterpret_cast<const bf8*>(qp + d * 2);
-        qb[q][0][i / 8] = t;
-      } else {
+      for (int i = 0; i < D / 4; i += BF ? 8 : 4) {
+        const int c = i / KW, d = 4 * KW * c + KW * g + i % KW;
+        if constexpr (BF && sizeof(IO) == 2) {
+          bf8 t = {};
+          if (row_ok) t = *reinterpret_cast<const bf8*>(qp + d * 2);
+          qb[q][0][i / 8] = t;
+        } else {
 #pragma unroll
-        for (int k = 0; k < (BF ? 8 : 4); k += 4) {
-          f4 t = {};
-          if (row_ok) t = *reinterpret_cast<const f4*>(qp + (d + k) * 4);
+          for (int k = 0; k < (BF ? 8 : 4); k += 4) {
+            f4 t = {};
+            if (row_ok) t = *reinterpret_cast<const f4*>(qp + (d + k) * 4);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if constexpr (BF) {
-              float rest = t[e];
+            for (int e = 0; e < 4; ++e) {
+              if constexpr (BF) {
+                // cut off, not rounded, so that the largest values stay finite
+                float rest = t[e];
 #pragma unroll
-              for (int n = 0; n < QT; ++n) {
-                qb[q][n][i / 8][k + e] = (__bf16)rest;
-                rest -= (float)qb[q][n][i / 8][k + e];
+                for (int n = 0; n < QT; ++n) {
+                  const float term = __uint_as_float(__float_as_uint(rest) & 0xffff0000u);
+                  qb[q][n][i / 8][k + e] = (__bf16)(fabsf(rest) < __builtin_inff() ? term : rest);
+                  rest = fabsf(rest) < __builtin_inff() ? rest - term : 0.f;
+                }
+              } else {
+                qf[q][i + e] = t[e];
               }
-            } else {
-              qf[q][i + e] = t[e];
             }
           }
         }
       }
     }
-  }
 
-  const char* kbase = (const char*)p.k + h * p.k_sh;
-  const char* vbase = (const char*)p.v + h * p.v_sh;
-  const int32_t* tab = p.table + b * p.table_stride;
+    const char* kbase = (const char*)p.k + h * p.k_sh;
+    const char* vbase = (const char*)p.v + h * p.v_sh;
+    const int32_t* tab = p.table + b * p.table_stride;
 
-  f4 acc[RT][NA];
-  float m[RT], l[RT];
-#pragma unroll
-  for (int q = 0; q < RT; ++q) {
-#pragma unroll
-    for (int i = 0; i < NA; ++i) acc[q][i] = f4{0.f, 0.f, 0.f, 0.f};
-    m[q] = -__builtin_inff();
-    l[q] = 0.f;
-  }
-
-  Raw<KW * ES> kr[NT][NC];
-  Raw<VW * ES> vr[NT][4][U];
-
-
-  // ---- page lookups
-  auto page_of = [&](int key) -> int { return (int)(((uint64_t)(uint32_t)key * p.page_mul) >> p.page_shift); };
-  // UNI: the table entries of a tile's subtiles (keys clamped into the row).
-  struct Ents { int e[NT]; };
-  auto load_ents = [&](int key0) {
-    Ents o;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) o.e[n] = tab[page_of(min(key0 + 16 * n, len - 1))];
-    return o;
-  };
-  // UNI: the resource of one subtile's rows of K or V: `rows` valid rows
-  // from its first (none for an entry outside the cache).
-  auto sub_rsrc = [&](const char* base, int64_t sp, uint32_t st, int ent, int key) {
-    const int off = key - page_of(key) * p.page_size;
-    const bool ok = ent >= 0 && ent < p.n_pages;
-    const int rows = ok ? min(16, len - key) : 0;
-    const uint32_t bytes = rows > 0 ? (uint32_t)(rows - 1) * st + D * ES : 0u;
-    return buf_rsrc_n(base + (ok ? (int64_t)ent * sp : 0) + (int64_t)off * st, bytes);
-  };
-  auto issue_k_uni = [&](const Ents& en, int key0) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const auto rs = sub_rsrc(kbase, p.k_sp, p.k_st, en.e[n], key0 + 16 * n);
-#pragma unroll
-      for (int c = 0; c < NC; ++c) kr[n][c] = raw_buf<KW * ES, ONCE>(rs, x * p.k_st + (4 * KW * c + KW * g) * ES);
-    }
-  };
-  auto issue_v_uni = [&](const Ents& en, int key0) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const auto rs = sub_rsrc(vbase, p.v_sp, p.v_st, en.e[n], key0 + 16 * n);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          vr[n][j][u] = raw_buf<VW * ES, ONCE>(rs, (4 * g + j) * p.v_st + (16 * VW * u + VW * x) * ES);
-    }
-  };
-  // Not UNI: lane l < KT looks up key l of a tile; `publish` leaves the byte
-  // offsets of its rows (kNone where there is no row) in this wave's LDS.
-  auto load_ent1 = [&](int key0) { return tab[page_of(min(key0 + min(lane, KT - 1), len - 1))]; };
-  auto publish = [&](int ent, int key0, int par) {
-    const int key = key0 + lane;
-    const int off = key - page_of(key) * p.page_size;
-    const bool ok = key < len && ent >= 0 && ent < p.n_pages;
-    if (lane < KT) {
-      offs[wave][par][0][lane] = ok ? (uint64_t)((int64_t)ent * p.k_sp + (int64_t)off * p.k_st) : kNone;
-      offs[wave][par][1][lane] = ok ? (uint64_t)((int64_t)ent * p.v_sp + (int64_t)off * p.v_st) : kNone;
-    }
-    __builtin_amdgcn_wave_barrier();
-  };
-  auto issue_k_any = [&](int par) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const uint64_t o = offs[wave][par][0][16 * n + x];
-      const char* src = kbase + (o == kNone ? 0 : o);  // no row: any row, masked below
-#pragma unroll
-      for (int c = 0; c < NC; ++c) kr[n][c] = raw_load<KW * ES, ONCE>(src + (4 * KW * c + KW * g) * ES);
-    }
-  };
-  uint32_t held = ~0u;  // bit 4n + j: key 16n + 4g + j has a row
-  auto issue_v_any = [&](int par) {
-    held = 0;
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint64_t o = offs[wave][par][1][16 * n + 4 * g + j];
-        held |= (o == kNone ? 0u : 1u) << (4 * n + j);
-        const char* src = vbase + (o == kNone ? 0 : o);
-#pragma unroll
-        for (int u = 0; u < U; ++u) vr[n][j][u] = raw_load<VW * ES, ONCE>(src + (16 * VW * u + VW * x) * ES);
-      }
-  };
-
-  Ents ent_cur = {}, ent_next = {};
-  int ent1_next = 0;
-  int par = 0;
-  if (c0 < c1) {
-    if constexpr (UNI) {
-      ent_cur = load_ents(c0);
-      issue_k_uni(ent_cur, c0);
-      ent_next = load_ents(c0 + KT);
-    } else {
-      publish(load_ent1(c0), c0, 0);
-      issue_k_any(0);
-      ent1_next = load_ent1(c0 + KT);
-    }
-  }
-  for (int key0 = c0; key0 < c1; key0 += KT) {
-    if constexpr (UNI) issue_v_uni(ent_cur, key0);
-    else issue_v_any(par);
-
-    // ---- scores of the tile
-    f4 s[RT][NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-      for (int q = 0; q < RT; ++q) s[q][n] = f4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        if constexpr (BF) {
-#pragma unroll
-          for (int w = 0; w < KW; w += 8) {
-            u32x4 t;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) t[i] = bf_pair<KE>(kr[n][c], w / 2 + i);
-#pragma unroll
-            for (int k = QT - 1; k >= 0; --k)
-#pragma unroll
-              for (int q = 0; q < RT; ++q)
-                s[q][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, t), qb[q][k][(c * KW + w) / 8],
-                                                                  s[q][n], 0, 0, 0);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < KW / 2; ++i) {
-            const f2 t = f_pair(kr[n][c], i);
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-              for (int q = 0; q < RT; ++q)
-                s[q][n] = __builtin_amdgcn_mfma_f32_16x16x4f32(t[e], qf[q][c * KW + 2 * i + e], s[q][n], 0, 0, 0);
-          }
-        }
-      }
-    }
-    // The next tile's keys into the registers that the scores just read.
-    uint32_t sub_ok = ~0u;
-    if constexpr (UNI) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        if (ent_cur.e[n] < 0 || ent_cur.e[n] >= p.n_pages) sub_ok &= ~(1u << n);
-      if (key0 + KT < c1) issue_k_uni(ent_next, key0 + KT);
-      ent_cur = ent_next;
-      ent_next = load_ents(key0 + 2 * KT);
-    } else {
-      par ^= 1;
-      if (key0 + KT < c1) {
-        publish(ent1_next, key0 + KT, par);
-        issue_k_any(par);
-        ent1_next = load_ent1(key0 + 2 * KT);
-      }
-    }
-
-    // ---- masks, running maximum, weights
+    f4 acc[RT][NA];
+    float m[RT], l[RT];
 #pragma unroll
     for (int q = 0; q < RT; ++q) {
-      float mx = m[q];
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int key = key0 + 16 * n + 4 * g + j;
-          const bool sees = key < lim[q] && (UNI ? ((sub_ok >> n) & 1) != 0 : ((held >> (4 * n + j)) & 1) != 0);
-          s[q][n][j] = sees ? s[q][n][j] * s_scale : -__builtin_inff();
-          mx = fmaxf(mx, s[q][n][j]);
-        }
-      mx = max_over_g(mx);
-      const float mu = mx == -__builtin_inff() ? 0.f : mx;
-      const float alpha = exp2_hw(m[q] - mu);
-      if (__any(mx != m[q])) {
-        l[q] *= alpha;
-#pragma unroll
-        for (int i = 0; i < NA; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[q][i][j] *= alpha;
-      }
-      m[q] = mx;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          s[q][n][j] = exp2_hw(s[q][n][j] - mu);
-          l[q] += s[q][n][j];
-        }
-    }
-    if constexpr (!UNI) {  // a row that is not there must not reach the product
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (!((held >> (4 * n + j)) & 1))
-#pragma unroll
-            for (int u = 0; u < U; ++u) vr[n][j][u] = {};
+      for (int i = 0; i < NA; ++i) acc[q][i] = f4{0.f, 0.f, 0.f, 0.f};
+      m[q] = -__builtin_inff();
+      l[q] = 0.f;
     }
 
-    // ---- output += weights x values.  A lane's weights of keys that its row
-    // does not see are zero, but zero times an infinity or NaN is not: in a
-    // tile where rows see different keys (T > 1, the row's last tokens) and
-    // such a value is present, each token takes the product on its own, with
-    // the values that it does not see replaced by zeros.
-    bool apart = false;
-    if (MT && key0 + KT > len - p.T + 1) {
-      bool odd = false;
+    Raw<KW * ES> kr[NT][NC];
+    Raw<VW * ES> vr[NT][4][U];
+
+
+    // ---- page lookups
+    auto page_of = [&](int key) -> int { return (int)(((uint64_t)(uint32_t)key * p.page_mul) >> p.page_shift); };
+    // UNI: the table entries of a tile's subtiles (keys clamped into the row).
+    struct Ents { int e[NT]; };
+    auto load_ents = [&](int key0) {
+      Ents o;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n) o.e[n] = tab[page_of(min(key0 + 16 * n, len - 1))];
+      return o;
+    };
+    // UNI: the resource of one subtile's rows of K or V: `rows` valid rows
+    // from its first (none for an entry outside the cache).
+    auto sub_rsrc = [&](const char* base, int64_t sp, uint32_t st, int ent, int key) {
+      const int off = key - page_of(key) * p.page_size;
+      const bool ok = ent >= 0 && ent < p.n_pages;
+      const int rows = ok ? min(16, len - key) : 0;
+      const uint32_t bytes = rows > 0 ? (uint32_t)(rows - 1) * st + D * ES : 0u;
+      return buf_rsrc_n(base + (ok ? (int64_t)ent * sp : 0) + (int64_t)off * st, bytes);
+    };
+    auto issue_k_uni = [&](const Ents& en, int key0) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const auto rs = sub_rsrc(kbase, p.k_sp, p.k_st, en.e[n], key0 + 16 * n);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) kr[n][c] = raw_buf<KW * ES, ONCE>(rs, x * p.k_st + (4 * KW * c + KW * g) * ES);
+      }
+    };
+    auto issue_v_uni = [&](const Ents& en, int key0) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const auto rs = sub_rsrc(vbase, p.v_sp, p.v_st, en.e[n], key0 + 16 * n);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int u = 0; u < U; ++u)
+            vr[n][j][u] = raw_buf<VW * ES, ONCE>(rs, (4 * g + j) * p.v_st + (16 * VW * u + VW * x) * ES);
+      }
+    };
+    // Not UNI: lane l < KT looks up key l of a tile; `publish` leaves the byte
+    // offsets of its rows (kNone where there is no row) in this wave's LDS.
+    auto load_ent1 = [&](int key0) { return tab[page_of(min(key0 + min(lane, KT - 1), len - 1))]; };
+    auto publish = [&](int ent, int key0, int par) {
+      const int key = key0 + lane;
+      const int off = key - page_of(key) * p.page_size;
+      const bool ok = key < len && ent >= 0 && ent < p.n_pages;
+      if (lane < KT) {
+        offs[wave][par][0][lane] = ok ? (uint64_t)((int64_t)ent * p.k_sp + (int64_t)off * p.k_st) : kNone;
+        offs[wave][par][1][lane] = ok ? (uint64_t)((int64_t)ent * p.v_sp + (int64_t)off * p.v_st) : kNone;
+      }
+      __builtin_amdgcn_wave_barrier();
+    };
+    auto issue_k_any = [&](int par) {
 #pragma unroll
-            for (int e = 0; e < VW / 2; ++e) {
-              if constexpr (BF) {
-                const uint32_t w = bf_pair<KE>(vr[n][j][u], e);
-                odd |= (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
-              } else {
-                const f2 w = f_pair(vr[n][j][u], e);
-                odd |= (__float_as_uint(w[0]) & 0x7f800000u) == 0x7f800000u ||
-                       (__float_as_uint(w[1]) & 0x7f800000u) == 0x7f800000u;
-              }
-            }
-      apart = __any(odd);
+      for (int n = 0; n < NT; ++n) {
+        const uint64_t o = offs[wave][par][0][16 * n + x];
+        const char* src = kbase + (o == kNone ? 0 : o);  // no row: any row, masked below
+#pragma unroll
+        for (int c = 0; c < NC; ++c) kr[n][c] = raw_load<KW * ES, ONCE>(src + (4 * KW * c + KW * g) * ES);
+      }
+    };
+    uint32_t held = ~0u;  // bit 4n + j: key 16n + 4g + j has a row
+    auto issue_v_any = [&](int par) {
+      held = 0;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint64_t o = offs[wave][par][1][16 * n + 4 * g + j];
+          held |= (o == kNone ? 0u : 1u) << (4 * n + j);
+          const char* src = vbase + (o == kNone ? 0 : o);
+#pragma unroll
+          for (int u = 0; u < U; ++u) vr[n][j][u] = raw_load<VW * ES, ONCE>(src + (16 * VW * u + VW * x) * ES);
+        }
+    };
+
+    Ents ent_cur = {}, ent_next = {};
+    int ent1_next = 0;
+    int par = 0;
+    if (c0 < c1) {
+      if constexpr (UNI) {
+        ent_cur = load_ents(c0);
+        issue_k_uni(ent_cur, c0);
+        ent_next = load_ents(c0 + KT);
+      } else {
+        publish(load_ent1(c0), c0, 0);
+        issue_k_any(0);
+        ent1_next = load_ent1(c0 + KT);
+      }
     }
-    if constexpr (BF) {
-      constexpr int NP = NT > 1 ? 2 : 1;  // subtiles of one product: 32 keys deep, or 16
+    for (int key0 = c0; key0 < c1; key0 += KT) {
+      if constexpr (UNI) issue_v_uni(ent_cur, key0);
+      else issue_v_any(par);
+
+      // ---- scores of the tile
+      f4 s[RT][NT];
 #pragma unroll
-      for (int a = 0; a < NT; a += NP) {
-        bf4 pw[RT][PT][NP];  // the weights' bf16 terms, largest first
+      for (int n = 0; n < NT; ++n) {
 #pragma unroll
-        for (int q = 0; q < RT; ++q)
+        for (int q = 0; q < RT; ++q) s[q][n] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int i = 0; i < NP; ++i)
+        for (int c = 0; c < NC; ++c) {
+          if constexpr (BF) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float rest = s[q][a + i][j];
+            for (int w = 0; w < KW; w += 8) {
+              u32x4 t;
 #pragma unroll
-              for (int k = 0; k < PT; ++k) {
-                pw[q][k][i][j] = (__bf16)rest;
-                rest -= (float)pw[q][k][i][j];
-              }
+              for (int i = 0; i < 4; ++i) t[i] = bf_pair<KE>(kr[n][c], w / 2 + i);
+#pragma unroll
+              for (int k = QT - 1; k >= 0; --k)
+#pragma unroll
+                for (int q = 0; q < RT; ++q)
+                  s[q][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, t), qb[q][k][(c * KW + w) / 8],
+                                                                    s[q][n], 0, 0, 0);
             }
+          } else {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+            for (int i = 0; i < KW / 2; ++i) {
+              const f2 t = f_pair(kr[n][c], i);
 #pragma unroll
-          for (int e2 = 0; e2 < VW / 2; ++e2) {
-            uint32_t c[4 * NP];
+              for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int j = 0; j < 4 * NP; ++j) c[j] = bf_pair<KE>(vr[a + (j >> 2)][j & 3][u], e2);
-            // V^T's operand for the pieces' lower or upper elements
-            auto dims = [&](const uint32_t* cc, int half, bf4* t) {
+                for (int q = 0; q < RT; ++q)
+                  s[q][n] = __builtin_amdgcn_mfma_f32_16x16x4f32(t[e], qf[q][c * KW + 2 * i + e], s[q][n], 0, 0, 0);
+            }
+          }
+        }
+      }
+      // The next tile's keys into the registers that the scores just read.
+      uint32_t sub_ok = ~0u;
+      if constexpr (UNI) {
 #pragma unroll
-              for (int i = 0; i < NP; ++i) {
-                uint2 w;
-                w.x = __builtin_amdgcn_perm(cc[4 * i + 1], cc[4 * i], half ? 0x07060302u : 0x05040100u);
-                w.y = __builtin_amdgcn_perm(cc[4 * i + 3], cc[4 * i + 2], half ? 0x07060302u : 0x05040100u);
-                t[i] = __builtin_bit_cast(bf4, w);
+        for (int n = 0; n < NT; ++n)
+          if (ent_cur.e[n] < 0 || ent_cur.e[n] >= p.n_pages) sub_ok &= ~(1u << n);
+        if (key0 + KT < c1) issue_k_uni(ent_next, key0 + KT);
+        ent_cur = ent_next;
+        ent_next = load_ents(key0 + 2 * KT);
+      } else {
+        par ^= 1;
+        if (key0 + KT < c1) {
+          publish(ent1_next, key0 + KT, par);
+          issue_k_any(par);
+          ent1_next = load_ent1(key0 + 2 * KT);
+        }
+      }
+
+      // ---- masks, running maximum, weights
+#pragma unroll
+      for (int q = 0; q < RT; ++q) {
+        float mx = m[q];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int key = key0 + 16 * n + 4 * g + j;
+            const bool sees = key < lim[q] && (UNI ? ((sub_ok >> n) & 1) != 0 : ((held >> (4 * n + j)) & 1) != 0);
+            s[q][n][j] = sees ? s[q][n][j] * s_scale : -__builtin_inff();
+            mx = fmaxf(mx, s[q][n][j]);
+          }
+        mx = max_over_g(mx);
+        const float mu = mx == -__builtin_inff() ? 0.f : mx;
+        const float alpha = exp2_hw(m[q] - mu);
+        if (__any(mx != m[q])) {
+          l[q] *= alpha;
+#pragma unroll
+          for (int i = 0; i < NA; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[q][i][j] *= alpha;
+        }
+        m[q] = mx;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            s[q][n][j] = exp2_hw(s[q][n][j] - mu);
+            l[q] += s[q][n][j];
+          }
+      }
+      if constexpr (!UNI) {  // a row that is not there must not reach the product
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (!((held >> (4 * n + j)) & 1))
+#pragma unroll
+              for (int u = 0; u < U; ++u) vr[n][j][u] = {};
+      }
+
+      // ---- output += weights x values.  A lane's weights of keys that its row
+      // does not see are zero, but zero times an infinity or NaN is not: in a
+      // tile where rows see different keys (T > 1, the row's last tokens) and
+      // such a value is present, each token takes the product on its own, with
+      // the values that it does not see replaced by zeros.
+      bool apart = false;
+      if (MT && key0 + KT > len - p.T + 1) {
+        bool odd = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+              for (int e = 0; e < VW / 2; ++e) {
+                if constexpr (BF) {
+                  const uint32_t w = bf_pair<KE>(vr[n][j][u], e);
+                  odd |= (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+                } else {
+                  const f2 w = f_pair(vr[n][j][u], e);
+                  odd |= (__float_as_uint(w[0]) & 0x7f800000u) == 0x7f800000u ||
+                         (__float_as_uint(w[1]) & 0x7f800000u) == 0x7f800000u;
+                }
               }
-            };
-            auto product = [&](const bf4* t, int q, int k, f4 in) {
-              if constexpr (NP == 2) return mma_k32(in, t[0], t[1], pw[q][k][0], pw[q][k][1]);
-              else return mma_k16(in, t[0], pw[q][k][0]);
-            };
-            if (!MT || !apart) {
-              bf4 t[2][NP];
-              dims(c, 0, t[0]);
-              dims(c, 1, t[1]);
+        apart = __any(odd);
+      }
+      if constexpr (BF) {
+        constexpr int NP = NT > 1 ? 2 : 1;  // subtiles of one product: 32 keys deep, or 16
 #pragma unroll
-              for (int k = PT - 1; k >= 0; --k)  // the terms outside: neighbouring products are independent
+        for (int a = 0; a < NT; a += NP) {
+          bf4 pw[RT][PT][NP];  // the weights' bf16 terms, largest first
+#pragma unroll
+          for (int q = 0; q < RT; ++q)
+#pragma unroll
+            for (int i = 0; i < NP; ++i)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                float rest = s[q][a + i][j];
+#pragma unroll
+                for (int k = 0; k < PT; ++k) {
+                  pw[q][k][i][j] = (__bf16)rest;
+                  rest -= (float)pw[q][k][i][j];
+                }
+              }
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e2 = 0; e2 < VW / 2; ++e2) {
+              uint32_t c[4 * NP];
+#pragma unroll
+              for (int j = 0; j < 4 * NP; ++j) c[j] = bf_pair<KE>(vr[a + (j >> 2)][j & 3][u], e2);
+              // V^T's operand for the pieces' lower or upper elements
+              auto dims = [&](const uint32_t* cc, int half, bf4* t) {
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                  uint2 w;
+                  w.x = __builtin_amdgcn_perm(cc[4 * i + 1], cc[4 * i], half ? 0x07060302u : 0x05040100u);
+                  w.y = __builtin_amdgcn_perm(cc[4 * i + 3], cc[4 * i + 2], half ? 0x07060302u : 0x05040100u);
+                  t[i] = __builtin_bit_cast(bf4, w);
+                }
+              };
+              auto product = [&](const bf4* t, int q, int k, f4 in) {
+                if constexpr (NP == 2) return mma_k32(in, t[0], t[1], pw[q][k][0], pw[q][k][1]);
+                else return mma_k16(in, t[0], pw[q][k][0]);
+              };
+              if (!MT || !apart) {
+                bf4 t[2][NP];
+                dims(c, 0, t[0]);
+                dims(c, 1, t[1]);
+#pragma unroll
+                for (int k = PT - 1; k >= 0; --k)  // the terms outside: neighbouring products are independent
+#pragma unroll
+                  for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int q = 0; q < RT; ++q) {
+                      f4& o = acc[q][u * VW + 2 * e2 + half];
+                      o = product(t[half], q, k, o);
+                    }
+              } else {
 #pragma unroll
                 for (int half = 0; half < 2; ++half)
 #pragma unroll
                   for (int q = 0; q < RT; ++q) {
                     f4& o = acc[q][u * VW + 2 * e2 + half];
-                    o = product(t[half], q, k, o);
+                    const f4 in = o;
+                    for (int t = 0; t < p.T; ++t) {
+                      uint32_t cz[4 * NP];
+#pragma unroll
+                      for (int j = 0; j < 4 * NP; ++j)
+                        cz[j] = key0 + 16 * (a + (j >> 2)) + 4 * g + (j & 3) < len - p.T + t + 1 ? c[j] : 0u;
+                      bf4 tz[NP];
+                      dims(cz, half, tz);
+                      f4 got = in;
+#pragma unroll
+                      for (int k = PT - 1; k >= 0; --k) got = product(tz, q, k, got);
+                      if (t == t_row[q]) o = got;
+                    }
                   }
-            } else {
+              }
+            }
+        }
+      } else {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e2 = 0; e2 < VW / 2; ++e2) {
+              f2 c[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) c[j] = f_pair(vr[n][j][u], e2);
 #pragma unroll
               for (int half = 0; half < 2; ++half)
 #pragma unroll
                 for (int q = 0; q < RT; ++q) {
                   f4& o = acc[q][u * VW + 2 * e2 + half];
-                  const f4 in = o;
-                  for (int t = 0; t < p.T; ++t) {
-                    uint32_t cz[4 * NP];
+                  if (!MT || !apart) {
+                    o = mma_k16(o, f4{c[0][half], c[1][half], c[2][half], c[3][half]}, s[q][n]);
+                  } else {
+                    const f4 in = o;
+                    for (int t = 0; t < p.T; ++t) {
+                      f4 z;
 #pragma unroll
-                    for (int j = 0; j < 4 * NP; ++j)
-                      cz[j] = key0 + 16 * (a + (j >> 2)) + 4 * g + (j & 3) < len - p.T + t + 1 ? c[j] : 0u;
-                    bf4 tz[NP];
-                    dims(cz, half, tz);
-                    f4 got = in;
-#pragma unroll
-                    for (int k = PT - 1; k >= 0; --k) got = product(tz, q, k, got);
-                    if (t == t_row[q]) o = got;
+                      for (int j = 0; j < 4; ++j)
+                        z[j] = key0 + 16 * n + 4 * g + j < len - p.T + t + 1 ? c[j][half] : 0.f;
+                      const f4 got = mma_k16(in, z, s[q][n]);
+                      if (t == t_row[q]) o = got;
+                    }
                   }
                 }
             }
-          }
       }
-    } else {
+    }
+
+    // ---- results: the lane's query rows, VW neighbouring dimensions at a time
+    asm volatile("" : "+v"(own));
+    const int xo = own & 15, go = own >> 4;
+    constexpr int SW = VW < 4 ? VW : 4;
+    typedef float fs __attribute__((ext_vector_type(SW)));
+    typedef IO ios __attribute__((ext_vector_type(SW)));
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+    for (int q = 0; q < RT; ++q) {
+      const float lq = sum_over_g(l[q]);
+      const int ro = (rt * RT + q) * 16 + xo;
+      if (ro < p.R && !whole) {
+        const int64_t to = ((int64_t)slot * p.hkv + h) * p.R + ro;
+        float* o = p.part_o + to * D + VW * 4 * go;
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-          for (int e2 = 0; e2 < VW / 2; ++e2) {
-            f2 c[4];
+          for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) c[j] = f_pair(vr[n][j][u], e2);
+            for (int e = 0; e < VW; e += SW) {
+              fs w;
 #pragma unroll
-            for (int half = 0; half < 2; ++half)
+              for (int i = 0; i < SW; ++i) w[i] = acc[q][u * VW + e + i][j];
+              *reinterpret_cast<fs*>(o + 16 * VW * u + VW * j + e) = w;
+            }
+        if (go == 0) *reinterpret_cast<f2*>(p.part_ml + to * 2) = f2{m[q], lq};
+      } else if (ro < p.R) {
+        const int64_t row = ((int64_t)b * p.T + ro / p.group) * p.hq + h * p.group + ro % p.group;
+        IO* o = (IO*)p.out + row * D + VW * 4 * go;
+        const float inv = attn_inv(p, m[q], lq, h);
 #pragma unroll
-              for (int q = 0; q < RT; ++q) {
-                f4& o = acc[q][u * VW + 2 * e2 + half];
-                if (!MT || !apart) {
-                  o = mma_k16(o, f4{c[0][half], c[1][half], c[2][half], c[3][half]}, s[q][n]);
-                } else {
-                  const f4 in = o;
-                  for (int t = 0; t < p.T; ++t) {
-                    f4 z;
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                      z[j] = key0 + 16 * n + 4 * g + j < len - p.T + t + 1 ? c[j][half] : 0.f;
-                    const f4 got = mma_k16(in, z, s[q][n]);
-                    if (t == t_row[q]) o = got;
-                  }
-                }
-              }
-          }
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < VW; e += SW) {
+              ios w;
+#pragma unroll
+              for (int i = 0; i < SW; ++i) w[i] = from_f32<IO>(attn_out(acc[q][u * VW + e + i][j], m[q], inv));
+              *reinterpret_cast<ios*>(o + 16 * VW * u + VW * j + e) = w;
+            }
+        if (p.lse && go == 0) p.lse[row] = attn_lse(m[q], lq);
+      }
     }
-  }
-
-  // ---- results: the lane's query rows, VW neighbouring dimensions at a time
-  asm volatile("" : "+v"(own));
-  const int xo = own & 15, go = own >> 4;
-  constexpr int SW = VW < 4 ? VW : 4;
-  typedef float fs __attribute__((ext_vector_type(SW)));
-  typedef IO ios __attribute__((ext_vector_type(SW)));
-#pragma unroll
-  for (int q = 0; q < RT; ++q) {
-    const float lq = sum_over_g(l[q]);
-    const int ro = (rt * RT + q) * 16 + xo;
-    if (ro < p.R && !whole) {
-      const int64_t to = ((int64_t)slot * p.hkv + h) * p.R + ro;
-      float* o = p.part_o + to * D + VW * 4 * go;
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int e = 0; e < VW; e += SW) {
-            fs w;
-#pragma unroll
-            for (int i = 0; i < SW; ++i) w[i] = acc[q][u * VW + e + i][j];
-            *reinterpret_cast<fs*>(o + 16 * VW * u + VW * j + e) = w;
-          }
-      if (go == 0) *reinterpret_cast<f2*>(p.part_ml + to * 2) = f2{m[q], lq};
-    } else if (ro < p.R) {
-      const int64_t row = ((int64_t)b * p.T + ro / p.group) * p.hq + h * p.group + ro % p.group;
-      IO* o = (IO*)p.out + row * D + VW * 4 * go;
-      const float inv = attn_inv(p, m[q], lq, h);
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int e = 0; e < VW; e += SW) {
-            ios w;
-#pragma unroll
-            for (int i = 0; i < SW; ++i) w[i] = from_f32<IO>(attn_out(acc[q][u * VW + e + i][j], m[q], inv));
-            *reinterpret_cast<ios*>(o + 16 * VW * u + VW * j + e) = w;
-          }
-      if (p.lse && go == 0) p.lse[row] = attn_lse(m[q], lq);
-    }
-  }
   }
 }
 

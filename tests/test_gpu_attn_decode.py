@@ -298,6 +298,27 @@ def test_scores_far_apart_and_infinite():
     assert ((out.double().cpu() - top).abs() <= 2.0 ** -22 * top.abs()).all()
 
 
+@pytest.mark.parametrize("cache", ["f32", "e4m3"])
+def test_the_largest_queries(cache):
+    """The largest finite fp32 query keeps its sign and size; an infinite one
+    gives no number, as its scores' differences are none."""
+    lens = torch.tensor([40], dtype=torch.int32)
+    table, n_pages = paged(lens, 16)
+    kc, vc = caches(n_pages, 16, 1, 64, cache, seed=2)
+    kw = torch.zeros(kc.shape)
+    kw[..., 5] = 2.0 ** -9
+    kw[int(table[0, 1]), 7, 0, 5] = 2.0 ** -8
+    kc = kw.to(DT[cache])
+    one = torch.ones(1).cuda() if cache == "e4m3" else None
+    q = torch.zeros(1, 1, 3, 64)
+    q[0, 0, 0, 5], q[0, 0, 1, 5], q[0, 0, 2, 5] = 3.4028234e38, 3.3961e38, float("inf")
+    out = gdn.attn_decode(q.cuda(), kc.cuda(), vc.cuda(), table.cuda(), lens.cuda(), k_scale=one, v_scale=one).cpu()
+    want = vc[int(table[0, 1]), 7, 0].float()
+    # the weight is one key's: its value, within the division's and sum's roundings
+    assert ((out[0, 0, :2] - want).abs() <= 2.0 ** -22 * want.abs()).all()
+    assert out[0, 0, 2].isnan().all()
+
+
 def test_offsets_past_32_bits():
     """Pages whose element offset needs more than 32 bits."""
     n_pages, page, hkv, d = (1 << 21) + 64, 16, 1, 64  # 2^31 elements and some
