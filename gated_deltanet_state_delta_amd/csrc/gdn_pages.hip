@@ -200,21 +200,30 @@ __global__ void __launch_bounds__(256) extend_count_kernel(PagesParams p, const 
   __shared__ int lds[4];
   if ((int)blockIdx.x < p.tiles) return count_tile<false>(p, p.refs, p.refs_out != p.refs, lds);
   int64_t before = 0;
-  for (int r0 = 0; r0 < p.rows; r0 += 256) {
-    const int r = r0 + threadIdx.x;
-    int need = -1;
-    if (r < p.rows) {
-      const int len = row_len(p, p.lens, r);
-      const int64_t grown = (int64_t)len + max(add[r], 0);
-      if (grown <= (int64_t)p.max_pages * p.page_size) need = pages_of(p, (int)grown) - pages_of(p, len);
+  for (int r0 = 0; r0 < p.rows; r0 += 1024) {  // four neighbouring rows a thread
+    const int r = r0 + (int)threadIdx.x * 4;
+    int need[4], from[4], mine = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      need[k] = -1;
+      if (r + k < p.rows) {
+        const int len = row_len(p, p.lens, r + k);
+        const int64_t grown = (int64_t)len + max(add[r + k], 0);
+        if (grown <= (int64_t)p.max_pages * p.page_size) need[k] = pages_of(p, (int)grown) - pages_of(p, len);
+      }
+      // a sum past the pages' number counts as n_pages + 1 (n_pages is at most
+      // 2^22), so that the workgroup's sum stays below 2^31
+      from[k] = mine;
+      mine = min(mine + min(max(need[k], 0), p.n_pages + 1), p.n_pages + 1);
     }
-    // a need counts as n_pages + 1 at most, so that a step's 256 stay below 2^31
     int all;
-    const int at = block_before(min(max(need, 0), p.n_pages + 1), lds, all);
-    if (r < p.rows) {
-      p.row_a[r] = (int)min(before + at, (int64_t)p.n_pages + 1);
-      p.row_b[r] = need;
-    }
+    const int64_t at = before + block_before(mine, lds, all);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (r + k < p.rows) {
+        p.row_a[r + k] = (int)min(at + from[k], (int64_t)p.n_pages + 1);
+        p.row_b[r + k] = need[k];
+      }
     before = min(before + all, (int64_t)p.n_pages + 1);
   }
 }

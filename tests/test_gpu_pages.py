@@ -25,7 +25,8 @@ def _same(got, want):
 
 # rows, pages a row, page size, pages, pages shared by long rows
 SIZES = [(1, 1, 1, 1, 0), (1, 3, 16, 2, 0), (5, 4, 16, 21, 2), (7, 3, 1, 9, 0), (40, 9, 5, 300, 3),
-         (300, 17, 16, 1024, 1), (257, 40, 64, 5000, 0), (600, 12, 3, 4097, 2), (3, 700, 16, 1500, 5)]
+         (300, 17, 16, 1024, 1), (257, 40, 64, 5000, 0), (600, 12, 3, 4097, 2), (3, 700, 16, 1500, 5),
+         (2500, 6, 16, 9000, 1)]
 
 
 def _state(size, seed):
@@ -119,6 +120,20 @@ def test_lengths_and_entries_outside_their_range(call):
     ref = {"extend": extend_ref, "fork": fork_ref, "free": free_ref}[call]
     want = ref(table, lens.clamp(-1, 1 << 30), refs, [min(x, 99) if call != "free" else x for x in arg.tolist()], 8)
     _same(getattr(gdn, "pages_" + call)(*_cuda(table, lens, refs, arg), 8), want)
+
+
+def test_needs_far_past_the_cache():
+    """Rows that need more pages than there are: they and those behind them
+    that need any are not served, the others are."""
+    rows, n = 1300, 1000
+    table = torch.full((rows, 64), -1, dtype=torch.int32)
+    lens, refs = torch.zeros(rows, dtype=torch.int32), torch.zeros(n, dtype=torch.int32)
+    r = random.Random(4)
+    add = torch.tensor([r.choice([0, 0, 0, 1, 1]) for _ in range(rows)], dtype=torch.int32)
+    add[700:] = torch.tensor([r.choice([0, 1, 64]) for _ in range(rows - 700)], dtype=torch.int32)
+    want = extend_ref(table, lens, refs, add, 1)
+    assert 0 < sum(want[3]) < rows
+    _same(gdn.pages_extend(*_cuda(table, lens, refs, add), 1), want)
 
 
 def test_strided_tables():
