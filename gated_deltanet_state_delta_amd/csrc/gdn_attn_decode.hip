@@ -8,10 +8,10 @@ namespace gdn {
 // sum_s e^{m_s - M} l_s.  Latency-bound: WPR waves take its parts in turn,
 // eight loads in flight each, the weights in the lanes of one wave.  A row's
 // parts: slot 2k + 1 of its first share k, then slots 2k of the shares behind.
-// Four waves a row (joined through LDS) where rows are few and their parts
-// many, one where rows are many.
+// The fewer the rows, the more parts each has: sixteen waves a row (joined
+// through LDS) up to 256 rows, four up to 1024, one beyond.
 template <typename IO, int D, int WPR>
-__global__ void __launch_bounds__(256) attn_join_kernel(AttnParams p) {
+__global__ void __launch_bounds__(WPR > 1 ? 64 * WPR : 256) attn_join_kernel(AttnParams p) {
   constexpr int V = D < 64 ? 1 : D / 64;  // dimensions of a lane (the first 32 lanes' for D = 32)
   __shared__ float red[WPR > 1 ? WPR : 1][64 * V];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -84,7 +84,8 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnParams p) {
 template <typename IO, int D>
 static void launch_join_d(const AttnParams& p, hipStream_t stream) {
   const int64_t rows = (int64_t)p.batch * p.hkv * p.R;
-  if (rows <= 1024) hipLaunchKernelGGL((attn_join_kernel<IO, D, 4>), dim3((unsigned)rows), dim3(256), 0, stream, p);
+  if (rows <= 256) hipLaunchKernelGGL((attn_join_kernel<IO, D, 16>), dim3((unsigned)rows), dim3(1024), 0, stream, p);
+  else if (rows <= 1024) hipLaunchKernelGGL((attn_join_kernel<IO, D, 4>), dim3((unsigned)rows), dim3(256), 0, stream, p);
   else hipLaunchKernelGGL((attn_join_kernel<IO, D, 1>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, p);
 }
 template <typename IO>
