@@ -231,11 +231,17 @@ def attn_decode_workspace_size(q, k_cache, v_cache, page_table, lens, **kw) -> i
 
 
 def _tokens(x, shape):
-    """[B, T, hkv, d] as rows of tokens one stride apart: x itself where it is
-    so laid out (the stride before the last two is then the tokens')."""
+    """[B, T, hkv, d] as rows of tokens one stride apart: x itself where it is dense."""
     if x.is_contiguous():
         return x
     return x.reshape(shape[0] * shape[1], shape[2], shape[3])
+
+
+def _token_strides(x, hkv, d):
+    """Token and head strides of what _tokens gives.  A contiguous tensor's
+    dimensions of one entry may carry any stride (a step of a sequence-first
+    buffer: T's is that of the steps), so its strides are taken from its shape."""
+    return (hkv * d, d) if x.is_contiguous() else x.stride()[-3:-1]
 
 
 def kv_append_args(k, v, k_cache, v_cache, page_table, lens, *, cu_seqlens=None, k_scale=None, v_scale=None):
@@ -264,9 +270,9 @@ def kv_append_args(k, v, k_cache, v_cache, page_table, lens, *, cu_seqlens=None,
     k, v = _rows16(k), _rows16(v)
     table, table_stride, max_pages = _table(page_table, B)
     lens = _i32(lens, "lens", (B,))
-    ks, vs = k.stride(), v.stride()
     a = _lib.KvAppendArgs(
-        total, B, hkv, d, _IO[dtype], cache_dtype, k.data_ptr(), ks[-3], ks[-2], v.data_ptr(), vs[-3], vs[-2],
+        total, B, hkv, d, _IO[dtype], cache_dtype, k.data_ptr(), *_token_strides(k, hkv, d),
+        v.data_ptr(), *_token_strides(v, hkv, d),
         _ptr(cu_seqlens), k_cache.data_ptr(), *kcs, v_cache.data_ptr(), *vcs, cs[0], cs[1], max_pages,
         table.data_ptr(), table_stride, lens.data_ptr(), _ptr(k_scale), _ptr(v_scale))
     return a, (k, v, cu_seqlens, table, lens, k_scale, v_scale)

@@ -155,3 +155,24 @@ def test_nothing_to_write():
     gdn.kv_append(k, k, kc, vc, torch.zeros(1, 1, dtype=torch.int32).cuda(), torch.ones(1, dtype=torch.int32).cuda(),
                   cu_seqlens=torch.zeros(2, dtype=torch.int32).cuda())
     assert torch.equal(kc, before)
+
+
+@pytest.mark.parametrize("rows,hkv", [(64, 4), (3, 1), (1, 2)])
+@pytest.mark.parametrize("io,cache", [("bf16", "bf16"), ("f32", "f32"), ("f32", "e4m3")])
+def test_steps_of_a_sequence_first_buffer(io, cache, rows, hkv):
+    """[B, 1, hkv, d] views of [steps, B, hkv, d]: contiguous to torch, with the
+    steps' stride in the dimension of one token."""
+    lens = [b % 30 + 1 for b in range(rows)]
+    table, n_pages = paged(lens, 16, seed=rows)
+    kc, vc = caches(n_pages, 16, hkv, 64, cache, seed=rows)
+    g = torch.Generator().manual_seed(rows)
+    k, v = (torch.randn(3, rows, hkv, 64, generator=g).to(DT[io]) for _ in range(2))
+    s = torch.rand(hkv, generator=g) * 0.02 + 0.001 if cache == "e4m3" else None
+    sd = None if s is None else s.cuda()
+    lens = torch.tensor(lens, dtype=torch.int32)
+    for i in range(3):
+        want = [_want(c, x[i], [1] * rows, table, lens, 16, s) for c, x in ((kc, k), (vc, v))]
+        step = [x.cuda()[i:i + 1].transpose(0, 1) for x in (k, v)]
+        got = gdn.kv_append(*step, kc.cuda(), vc.cuda(), table.cuda(), lens.cuda(), k_scale=sd, v_scale=sd)
+        for a, b in zip(got, want):
+            assert torch.equal(_bits(a), b)

@@ -246,3 +246,33 @@ def test_cpu_tensors_are_refused():
                  lambda: gdn.pages_compact(i32(2, 3), i32(5))):
         with pytest.raises(ValueError):
             call()
+
+
+def _with_strides(t, *strides):
+    """t's values with the strides of its dimensions of one entry replaced
+    (None: as they are); still contiguous to torch."""
+    t = torch.as_strided(t, t.shape, [s if n == 1 and s is not None else st for n, s, st in zip(t.shape, strides, t.stride())])
+    assert t.is_contiguous()
+    return t
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("rows,hkv", [(64, 4), (1, 4), (5, 1), (1, 1)])
+def test_kv_append_args_read_the_tokens_where_they_are(rows, hkv, packed):
+    """Dimensions of one entry carry any stride, also in a contiguous tensor: a
+    step of a sequence-first buffer is one, and its token stride is the rows'."""
+    d, dense = 64, (hkv * 64, 64)
+    steps = torch.zeros(3, rows, hkv, d)
+    if packed:
+        inputs = [torch.zeros(rows, hkv, d), _with_strides(torch.zeros(rows, hkv, d), 7, 13, 1)]
+    else:
+        inputs = [torch.zeros(rows, 1, hkv, d), steps[:1].transpose(0, 1), steps[1:2].transpose(0, 1),
+                  torch.zeros(1, rows, hkv, d).transpose(0, 1), _with_strides(torch.zeros(rows, 1, hkv, d), 7, 7, 13, 1)]
+    cache = torch.zeros(9, 16, hkv, d)
+    x = dict(k_cache=cache, v_cache=cache.clone(), page_table=torch.zeros(rows, 4, dtype=torch.int32),
+             lens=torch.zeros(rows, dtype=torch.int32), cu_seqlens=torch.arange(rows + 1, dtype=torch.int32) if packed else None)
+    for k in inputs:
+        for v in inputs:
+            a, keep = gdn.kv_append_args(k, v, **x)
+            assert (a.k, a.v, a.total_tokens) == (k.data_ptr(), v.data_ptr(), rows)
+            assert (a.k_stride_token, a.k_stride_head) == dense and (a.v_stride_token, a.v_stride_head) == dense
