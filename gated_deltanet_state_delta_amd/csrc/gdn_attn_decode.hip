@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(WPR > 1 ? 64 * WPR : 256) attn_join_kernel(Att
   if (lane * V < D) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const float out = attn_out(acc[v], m, attn_inv(p, m, l, h));
+      const float out = attn_out(acc[v], l, attn_inv(p, l, h));
       if constexpr (sizeof(IO) == 2) ((__bf16*)p.out)[at * D + d + v] = (__bf16)out;
       else ((float*)p.out)[at * D + d + v] = out;
     }

@@ -125,15 +125,17 @@ __device__ __forceinline__ AttnShare attn_share(const AttnParams& p, int k, int 
   return r;
 }
 
-// One output: the weighted sum over the weights' sum.  A row that sees nothing
-// (maximum -inf) is zero.
-__device__ __forceinline__ float attn_inv(const AttnParams& p, float m, float l, int h) {
+// One output: the weighted sum over the weights' sum l.  l is at least 1 (the
+// largest score's weight) unless a row sees nothing or scores of -inf only: then
+// it is 0, and the output zero.  The maximum does not tell these rows from one
+// whose scores are all NaN (fmaxf drops NaN); there l is NaN and so is the output.
+__device__ __forceinline__ float attn_inv(const AttnParams& p, float l, int h) {
   return (p.v_scale ? p.v_scale[h] : 1.0f) / l;
 }
-__device__ __forceinline__ float attn_out(float o, float m, float inv) { return m == -__builtin_inff() ? 0.f : o * inv; }
+__device__ __forceinline__ float attn_out(float o, float l, float inv) { return l == 0.f ? 0.f : o * inv; }
 // Natural log of the weights' sum, from the maximum and sum in units of log2.
 __device__ __forceinline__ float attn_lse(float m, float l) {
-  return m == -__builtin_inff() ? m : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
+  return l == 0.f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
 }
 
 // N raw bytes of a row piece, as dwords (2 bytes sit in the low half).
@@ -726,7 +728,7 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND>::OCC)) attn_dec
       } else if (ro < p.R) {
         const int64_t row = ((int64_t)b * p.T + ro / p.group) * p.hq + h * p.group + ro % p.group;
         IO* o = (IO*)p.out + row * D + VW * 4 * go;
-        const float inv = attn_inv(p, m[q], lq, h);
+        const float inv = attn_inv(p, lq, h);
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -735,7 +737,7 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND>::OCC)) attn_dec
             for (int e = 0; e < VW; e += SW) {
               ios w;
 #pragma unroll
-              for (int i = 0; i < SW; ++i) w[i] = from_f32<IO>(attn_out(acc[q][u * VW + e + i][j], m[q], inv));
+              for (int i = 0; i < SW; ++i) w[i] = from_f32<IO>(attn_out(acc[q][u * VW + e + i][j], lq, inv));
               *reinterpret_cast<ios*>(o + 16 * VW * u + VW * j + e) = w;
             }
         if (p.lse && go == 0) p.lse[row] = attn_lse(m[q], lq);

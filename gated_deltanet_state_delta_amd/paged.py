@@ -194,8 +194,9 @@ def attn_decode(q, k_cache, v_cache, page_table, lens, *, scale=None, k_scale=No
     position lens[b] - T + t and sees the positions up to its own.  Query head
     h reads key-value head h*hkv//hq.  scale None means 1/sqrt(d).
 
-    Rows or tokens that see nothing (lens 0, table entries outside the cache)
-    get zeros and lse -inf.  Rows may share pages.  return_lse: also return
+    Rows or tokens that see nothing (lens 0, table entries outside the cache),
+    or whose scores are all -inf, get zeros and lse -inf; NaN in a query or in a
+    key that it sees gives NaN.  Rows may share pages.  return_lse: also return
     log sum exp of the scores, [B, T, hq] float32, to join the result with
     attention over other keys.  workspace: a uint8 CUDA tensor of at least
     attn_decode_workspace_size bytes for the split over the rows' lengths;

@@ -444,8 +444,10 @@ gdn_status gdn_conv1d(const gdn_conv1d_args* args, void* stream);
  *     out[b,t,h] = v_scale[g] * sum_j e^{s_j} V[b,j,g] / sum_j e^{s_j}
  *     lse[b,t,h] = log sum_j e^{s_j}
  * A token that sees nothing (a row of no tokens, a position below 0, only
- * invalid pages) gets zeros and lse -inf.  Values at positions that a token
- * does not see never reach its result, infinities and NaN included.  Sums and
+ * invalid pages), or whose scores are all -inf, gets zeros and lse -inf.  A NaN
+ * in a token's query or in a key that it sees makes its result and lse NaN.
+ * Values at positions that a token does not see never reach its result,
+ * infinities and NaN included.  Sums and
  * the softmax are fp32; bf16 weights enter the product as two bf16 terms.
  *
  *   q    [batch, T, hq, d] io_dtype, strides {row, token, head}

@@ -401,3 +401,81 @@ def test_other_stream_and_captured_graphs():
     graphs[0].replay()
     torch.cuda.synchronize()
     assert torch.equal(outs[0], gdn.attn_decode(qs[0], kc, vc, table, n))
+
+
+# T, query heads a key-value head: one row of a head, several tokens, two row tiles, more
+ROWS = [(1, 2), (3, 2), (3, 8), (5, 9)]
+
+
+@pytest.mark.parametrize("page", [16, 5])
+@pytest.mark.parametrize("T,group", ROWS)
+@pytest.mark.parametrize("io,cache", [("bf16", "bf16"), ("f32", "f32"), ("bf16", "e4m3"), ("f32", "e4m3")])
+def test_a_nan_query_gives_nan(io, cache, T, group, page):
+    """NaN in the query of one head of one token of each row: that head's
+    result and lse are NaN, every other as without it.  Rows walked whole and
+    rows that are split and joined, the last one seeing nothing."""
+    lens = torch.tensor([T + 20, 700, 0], dtype=torch.int32)
+    table, n_pages = paged(lens, page, seed=T)
+    kc, vc = caches(n_pages, page, 2, 64, cache, seed=T + group)
+    ks, vs = _scales(cache, 2)
+    q = torch.randn(3, T, 2 * group, 64, generator=torch.Generator().manual_seed(T)).to(DT[io])
+    want, want_lse, mean, size = attn_ref(q, kc, vc, table, lens, 0.125, ks, vs)
+    odd = torch.zeros(3, T, 2 * group, dtype=torch.bool)
+    for b, (t, h) in enumerate([(0, 1), (T - 1, 2 * group - 1), (0, 0)]):
+        q[b, t, h, (b * 31 + 5) % 64] = float("nan")
+        odd[b, t, h] = b < 2
+    bound = attn_bound(want, mean, size, lens, 64, io)
+    tol = 2.0 ** -24 * ((64 + 16) * size[..., 0] + 32 * (want_lse.abs() + 16))
+    args = (q.cuda(), kc.cuda(), vc.cuda(), table.cuda(), lens.cuda())
+    for split in (True, False):
+        if split:
+            assert gdn.attn_decode_workspace_size(*args, k_scale=_dev(ks), v_scale=_dev(vs)) > 0
+            out, lse = gdn.attn_decode(*args, k_scale=_dev(ks), v_scale=_dev(vs), return_lse=True)
+        else:  # without a workspace one wave walks each row and head
+            lse = torch.empty(3, T, 2 * group, device="cuda")
+            a, keep, out = gdn.attn_decode_args(*args, k_scale=_dev(ks), v_scale=_dev(vs), lse=lse)
+            _lib.check(_lib.load().gdn_attn_decode(ctypes.byref(a), torch.cuda.current_stream().cuda_stream))
+        out, lse = out.double().cpu(), lse.double().cpu()
+        assert torch.equal(out.isnan(), odd[..., None].expand_as(out)) and torch.equal(lse.isnan(), odd)
+        assert ((out - want).abs() <= bound)[~odd].all()
+        assert torch.equal(lse == -float("inf"), (want_lse == -float("inf")) & ~odd)
+        seen = ~odd & (want_lse > -float("inf"))
+        assert ((lse - want_lse).abs() <= tol)[seen].all()
+
+
+@pytest.mark.parametrize("page", [16, 3])
+@pytest.mark.parametrize("T", [1, 2])
+@pytest.mark.parametrize("io,cache", [("bf16", "bf16"), ("f32", "f32"), ("bf16", "e4m3"), ("f32", "e4m3")])
+def test_keys_of_nan_and_scores_of_minus_infinity(io, cache, T, page):
+    """Rows whose only visible keys are NaN give NaN; rows whose scores are all
+    -inf give zeros and lse -inf; one NaN key among others gives NaN."""
+    lens = torch.tensor([1, 300, 300, 300], dtype=torch.int32)
+    table, n_pages = paged(lens, page, seed=1)
+    kc, vc = caches(n_pages, page, 1, 64, cache, seed=3)
+    kw = kc.float()
+
+    def put(b, at, value):
+        for j in at:
+            kw[int(table[b, j // page]), j % page] = value
+    put(0, [0], float("nan"))
+    put(1, range(300), float("nan"))
+    if cache == "e4m3":  # no infinities: the query's are the scores'
+        put(2, range(300), 2.0)
+    else:
+        put(2, range(300), -float("inf"))
+    put(3, [170], float("nan"))
+    q = torch.rand(4, T, 2, 64, generator=torch.Generator().manual_seed(2)) + 0.5
+    if cache == "e4m3":
+        q[2] = -float("inf")
+    q, kc = q.to(DT[io]), kw.to(kc.dtype)
+    one = torch.ones(1).cuda() if cache == "e4m3" else None
+    out, lse = gdn.attn_decode(q.cuda(), kc.cuda(), vc.cuda(), table.cuda(), lens.cuda(), k_scale=one, v_scale=one,
+                               return_lse=True)
+    out, lse = out.cpu(), lse.cpu()
+    # row 0 holds one token: the first of two new ones stands before it and sees nothing
+    if T == 2:
+        assert (out[0, 0] == 0).all() and (lse[0, 0] == -float("inf")).all()
+    assert out[0, -1].isnan().all() and lse[0, -1].isnan().all()
+    assert out[1].isnan().all() and lse[1].isnan().all()
+    assert (out[2] == 0).all() and (lse[2] == -float("inf")).all()
+    assert out[3].isnan().all() and lse[3].isnan().all()
