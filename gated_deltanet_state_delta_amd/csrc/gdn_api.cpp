@@ -307,8 +307,9 @@ static gdn_status cache_check(const char* f, int32_t batch, int32_t hkv, int32_t
                 hkv, d, n_pages, page_size, max_pages);
   if (d != 32 && d != 64 && d != 128 && d != 256)
     return fail(GDN_ERR_UNSUPPORTED, "%s: d=%d (supported: 32, 64, 128, 256)", f, d);
-  if ((int64_t)max_pages * page_size > (int64_t(1) << 30))
-    return fail(GDN_ERR_UNSUPPORTED, "%s: max_pages * page_size must be at most 2^30", f);
+  // page_size by itself too: max_pages may be 0
+  if (page_size > (1 << 30) || (int64_t)max_pages * page_size > (int64_t(1) << 30))
+    return fail(GDN_ERR_UNSUPPORTED, "%s: page_size and max_pages * page_size must be at most 2^30", f);
   if (table_stride < max_pages) return fail(GDN_ERR_LAYOUT, "%s: page_table_stride smaller than max_pages", f);
   if (cache_dtype == GDN_E4M3 && (!k_scale || !v_scale))
     return fail(GDN_ERR_NULL, "%s: an e4m3 cache needs k_scale and v_scale", f);

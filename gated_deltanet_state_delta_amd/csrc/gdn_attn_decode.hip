@@ -166,7 +166,7 @@ hipError_t launch_attn_decode(const gdn_attn_decode_args& a, hipStream_t stream)
   p.n_pages = a.n_pages;
   p.page_size = a.page_size;
   p.cap = a.max_pages * a.page_size;
-  // j / page_size for j < 2^31: with s = ceil(log2(page_size)) and
+  // j / page_size for j < 2^31 and page_size up to 2^30: with s = ceil(log2(page_size)) and
   // mul = ceil(2^(31 + s) / page_size), the error of mul is below 2^s.
   int s = 0;
   while ((1 << s) < a.page_size) ++s;

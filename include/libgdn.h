@@ -427,10 +427,10 @@ gdn_status gdn_conv1d(const gdn_conv1d_args* args, void* stream);
  *   lens        [batch] int32
  *   k_scale, v_scale  [hkv] fp32: the factor of each head's stored values,
  *               given for GDN_E4M3 caches and NULL for the others
- * Common requirements: max_pages * page_size at most 2^30; d in {32, 64, 128,
- * 256}; hq a multiple of hkv (query head h reads key-value head h*hkv/hq);
- * a cache has io_dtype's type or GDN_E4M3; caches, q, k, v and out 16-byte
- * aligned, their strides non-negative multiples of 16 bytes; a cache's token
+ * Common requirements: page_size and max_pages * page_size at most 2^30; d in
+ * {32, 64, 128, 256}; hq a multiple of hkv (query head h reads key-value head
+ * h*hkv/hq); a cache has io_dtype's type or GDN_E4M3; caches, q, k, v and out
+ * 16-byte aligned, their strides non-negative multiples of 16 bytes; a cache's token
  * and head strides in [d, 2^23) elements, its rows apart and its page stride
  * not smaller than a page.
  * ========================================================================= */

@@ -1,6 +1,9 @@
 """Refusals of the paged-cache calls on the host (no GPU needed): the C ABI's
 argument checks and the binding's shape checks, before anything is launched."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -9,6 +12,7 @@ import gated_deltanet_state_delta_amd as gdn
 import gated_deltanet_state_delta_amd._lib as L
 
 FAKE = 0x10000
+HERE = os.path.dirname(os.path.abspath(__file__))
 
 
 def _set(a, over):
@@ -276,3 +280,23 @@ def test_kv_append_args_read_the_tokens_where_they_are(rows, hkv, packed):
             a, keep = gdn.kv_append_args(k, v, **x)
             assert (a.k, a.v, a.total_tokens) == (k.data_ptr(), v.data_ptr(), rows)
             assert (a.k_stride_token, a.k_stride_head) == dense and (a.v_stride_token, a.v_stride_head) == dense
+
+
+def _alone(code):
+    """Runs code, which prints one number, in a process of its own: a call
+    that never returns or ends its process fails this test alone."""
+    head = "import ctypes, sys; sys.path[:0] = %r\nimport gated_deltanet_state_delta_amd._lib as L\n" \
+           "from test_paged_abi import _append, _attn\nlib = L.load()\n" % [HERE, os.path.dirname(HERE)]
+    res = subprocess.run([sys.executable, "-c", head + code], capture_output=True, text=True, timeout=100,
+                         env=dict(os.environ, HIP_VISIBLE_DEVICES=""))
+    assert res.returncode == 0, (res.returncode, res.stderr[-500:])
+    return [int(x) for x in res.stdout.split()]
+
+
+@pytest.mark.parametrize("page_size", [(1 << 30) + 1, (1 << 31) - 1])
+def test_page_sizes_past_their_limit_are_refused(page_size):
+    """Also where a table of no entries holds no positions."""
+    code = "for f, make in ((lib.gdn_attn_decode, _attn), (lib.gdn_kv_append, _append)):\n" \
+           "    for over in (dict(max_pages=0), dict(max_pages=0, n_pages=0), dict()):\n" \
+           "        print(f(ctypes.byref(make(page_size=%d, **over)), None))" % page_size
+    assert _alone(code) == [5] * 6
