@@ -295,10 +295,9 @@ gdn_status gdn_conv1d(const gdn_conv1d_args* p, void* stream) {
   return from_hip(gdn::launch_conv1d(a, (hipStream_t)stream), "gdn_conv1d launch");
 }
 
-// What the calls over a paged cache share: sizes, types and scales.
-static gdn_status cache_check(const char* f, int32_t batch, int32_t hkv, int32_t d, int32_t io_dtype,
-                              int32_t cache_dtype, int32_t n_pages, int32_t page_size, int32_t max_pages,
-                              int64_t table_stride, const float* k_scale, const float* v_scale) {
+// What the calls over a paged cache share: types and sizes.
+static gdn_status cache_sizes(const char* f, int32_t batch, int32_t hkv, int32_t d, int32_t io_dtype,
+                              int32_t cache_dtype, int32_t n_pages, int32_t page_size, int32_t max_pages) {
   if (io_dtype != GDN_F32 && io_dtype != GDN_BF16) return fail(GDN_ERR_DTYPE, "%s: io_dtype %d", f, io_dtype);
   if (cache_dtype != io_dtype && cache_dtype != GDN_E4M3)
     return fail(GDN_ERR_DTYPE, "%s: cache_dtype %d (io_dtype's type or GDN_E4M3)", f, cache_dtype);
@@ -310,6 +309,15 @@ static gdn_status cache_check(const char* f, int32_t batch, int32_t hkv, int32_t
   // page_size by itself too: max_pages may be 0
   if (page_size > (1 << 30) || (int64_t)max_pages * page_size > (int64_t(1) << 30))
     return fail(GDN_ERR_UNSUPPORTED, "%s: page_size and max_pages * page_size must be at most 2^30", f);
+  return GDN_OK;
+}
+
+// The same with the page table's stride and the scales.
+static gdn_status cache_check(const char* f, int32_t batch, int32_t hkv, int32_t d, int32_t io_dtype,
+                              int32_t cache_dtype, int32_t n_pages, int32_t page_size, int32_t max_pages,
+                              int64_t table_stride, const float* k_scale, const float* v_scale) {
+  const gdn_status st = cache_sizes(f, batch, hkv, d, io_dtype, cache_dtype, n_pages, page_size, max_pages);
+  if (st != GDN_OK) return st;
   if (table_stride < max_pages) return fail(GDN_ERR_LAYOUT, "%s: page_table_stride smaller than max_pages", f);
   if (cache_dtype == GDN_E4M3 && (!k_scale || !v_scale))
     return fail(GDN_ERR_NULL, "%s: an e4m3 cache needs k_scale and v_scale", f);
@@ -335,8 +343,34 @@ static gdn_status cache_layout(const char* f, const void* base, int64_t page, in
   return GDN_OK;
 }
 
+// The sizes that gdn_attn_decode takes beyond those of the caches.
+static gdn_status attn_sizes(const char* f, const gdn_attn_decode_args& a) {
+  if (a.T <= 0 || a.hq <= 0) return fail(GDN_ERR_SHAPE, "%s: bad sizes T=%d hq=%d", f, a.T, a.hq);
+  if (a.T > 64) return fail(GDN_ERR_UNSUPPORTED, "%s: T=%d (supported 1..64)", f, a.T);
+  if (a.hq % a.hkv != 0) return fail(GDN_ERR_SHAPE, "%s: hq=%d is not a multiple of hkv=%d", f, a.hq, a.hkv);
+  if (a.hq > 65536) return fail(GDN_ERR_UNSUPPORTED, "%s: hq=%d (supported up to 65536)", f, a.hq);
+  // Each size is below 2^31 and hq at most 2^16: in this order no product overflows 64 bits.
+  if ((int64_t)a.batch * a.hq >= (int64_t(1) << 31) || (int64_t)a.batch * a.hq * a.T >= (int64_t(1) << 31))
+    return fail(GDN_ERR_UNSUPPORTED, "%s: batch * hq * T must be below 2^31", f);
+  // one workgroup per row, key-value head and 16 query rows; a grid has at most 2^24 of 256 threads
+  if ((int64_t)a.batch * a.hkv * (((int64_t)a.T * (a.hq / a.hkv) + 15) / 16) > (int64_t(1) << 23))
+    return fail(GDN_ERR_UNSUPPORTED, "%s: batch * hkv * ceil(T * hq / hkv / 16) must be at most 2^23", f);
+  // the rows' tiles of 16 keys and more are counted in 32 bits
+  if ((int64_t)a.batch * (((int64_t)a.max_pages * a.page_size + 15) / 16 + 1) >= (int64_t(1) << 31))
+    return fail(GDN_ERR_UNSUPPORTED, "%s: batch * (max_pages * page_size / 16 + 1) must be below 2^31", f);
+  return GDN_OK;
+}
+
 size_t gdn_attn_decode_workspace_size(const gdn_attn_decode_args* args) {
-  return args ? gdn::attn_workspace_bytes(*args) : 0;
+  static const char* f = "gdn_attn_decode_workspace_size";
+  g_err[0] = 0;
+  if (!args) return 0;
+  const gdn_attn_decode_args& a = *args;
+  // the split's arithmetic holds for sizes that the call takes
+  if (cache_sizes(f, a.batch, a.hkv, a.d, a.io_dtype, a.cache_dtype, a.n_pages, a.page_size, a.max_pages) != GDN_OK ||
+      attn_sizes(f, a) != GDN_OK)
+    return 0;
+  return gdn::attn_workspace_bytes(a);
 }
 
 gdn_status gdn_attn_decode(const gdn_attn_decode_args* p, void* stream) {
@@ -347,20 +381,8 @@ gdn_status gdn_attn_decode(const gdn_attn_decode_args* p, void* stream) {
   gdn_status st = cache_check(f, a.batch, a.hkv, a.d, a.io_dtype, a.cache_dtype, a.n_pages, a.page_size, a.max_pages,
                               a.page_table_stride, a.k_scale, a.v_scale);
   if (st != GDN_OK) return st;
-  if (a.T <= 0 || a.hq <= 0) return fail(GDN_ERR_SHAPE, "%s: bad sizes T=%d hq=%d", f, a.T, a.hq);
-  if (a.T > 64) return fail(GDN_ERR_UNSUPPORTED, "%s: T=%d (supported 1..64)", f, a.T);
-  if (a.hq % a.hkv != 0) return fail(GDN_ERR_SHAPE, "%s: hq=%d is not a multiple of hkv=%d", f, a.hq, a.hkv);
-  if (a.hq > 65536) return fail(GDN_ERR_UNSUPPORTED, "%s: hq=%d (supported up to 65536)", f, a.hq);
-  if (a.batch == 0) return GDN_OK;
-  // Each size is below 2^31 and hq at most 2^16: in this order no product overflows 64 bits.
-  if ((int64_t)a.batch * a.hq >= (int64_t(1) << 31) || (int64_t)a.batch * a.hq * a.T >= (int64_t(1) << 31))
-    return fail(GDN_ERR_UNSUPPORTED, "%s: batch * hq * T must be below 2^31", f);
-  // one workgroup per row, key-value head and 16 query rows; a grid has at most 2^24 of 256 threads
-  if ((int64_t)a.batch * a.hkv * (((int64_t)a.T * (a.hq / a.hkv) + 15) / 16) > (int64_t(1) << 23))
-    return fail(GDN_ERR_UNSUPPORTED, "%s: batch * hkv * ceil(T * hq / hkv / 16) must be at most 2^23", f);
-  // the rows' tiles of 16 keys and more are counted in 32 bits
-  if ((int64_t)a.batch * (((int64_t)a.max_pages * a.page_size + 15) / 16 + 1) >= (int64_t(1) << 31))
-    return fail(GDN_ERR_UNSUPPORTED, "%s: batch * (max_pages * page_size / 16 + 1) must be below 2^31", f);
+  st = attn_sizes(f, a);
+  if (st != GDN_OK || a.batch == 0) return st;
   if (!a.q || !a.out || !a.lens || (a.max_pages > 0 && !a.page_table) || (a.n_pages > 0 && (!a.k_cache || !a.v_cache)))
     return fail(GDN_ERR_NULL, "%s: q, caches, page_table, lens and out are required", f);
   const size_t es = elem_size(a.io_dtype), ce = a.cache_dtype == GDN_E4M3 ? 1 : es;

@@ -125,8 +125,7 @@ static int attn_shares(const gdn_attn_decode_args& a) {
 }
 
 size_t attn_workspace_bytes(const gdn_attn_decode_args& a) {
-  if (a.batch <= 0 || a.T <= 0 || a.hkv <= 0 || a.hq < a.hkv || a.d <= 0 || a.max_pages <= 0 || a.page_size <= 0)
-    return 0;
+  if (a.batch == 0 || a.max_pages == 0) return 0;
   const int shares = attn_shares(a);
   if (shares == 0) return 0;
   return (2 * (size_t)shares * a.hq * a.T * (a.d + 2) + 2 * (size_t)a.batch) * sizeof(float);

@@ -8,7 +8,8 @@
 
 namespace gdn {
 
-// Workspace with which launch_attn_decode splits the rows (0: it does not).
+// Workspace with which launch_attn_decode splits the rows (0: it does not); sizes
+// already checked.
 size_t attn_workspace_bytes(const gdn_attn_decode_args& args);
 hipError_t launch_attn_decode(const gdn_attn_decode_args& args, hipStream_t stream);
 hipError_t launch_kv_append(const gdn_kv_append_args& args, hipStream_t stream);

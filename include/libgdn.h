@@ -463,7 +463,7 @@ gdn_status gdn_conv1d(const gdn_conv1d_args* args, void* stream);
  * 0 when none is of use) the rows' keys are dealt evenly to the waves of one
  * launch and the parts of a row joined by a second; with less, one wave walks
  * each row and key-value head: the same result up to rounding order.  The size
- * depends on sizes alone, not on lens.  The library keeps nothing in the
+ * depends on sizes alone, not on lens, and is 0 for sizes that the call refuses.  The library keeps nothing in the
  * workspace between calls; calls that share one must not overlap.
  * ------------------------------------------------------------------------- */
 typedef struct {

@@ -300,3 +300,16 @@ def test_page_sizes_past_their_limit_are_refused(page_size):
            "    for over in (dict(max_pages=0), dict(max_pages=0, n_pages=0), dict()):\n" \
            "        print(f(ctypes.byref(make(page_size=%d, **over)), None))" % page_size
     assert _alone(code) == [5] * 6
+
+
+def test_workspace_size_of_refused_sizes_is_zero():
+    """Sizes that gdn_attn_decode refuses need no workspace, and asking for one
+    ends no process."""
+    sizes = [dict(d=1 << 30, io_dtype=0, cache_dtype=0), dict(d=1 << 30), dict(d=1 << 28), dict(d=48), dict(d=(1 << 31) - 1),
+             dict(T=65536, hq=65536, hkv=1), dict(T=1 << 30), dict(T=65), dict(hq=1 << 30, T=4, hkv=1), dict(hq=7),
+             dict(page_size=(1 << 31) - 1, max_pages=(1 << 31) - 1, batch=(1 << 31) - 1), dict(batch=1 << 23, hq=512, hkv=2)]
+    code = "for over in %r:\n" \
+           "    a = _attn(**dict(dict(max_pages=9999, page_table_stride=9999), **over))\n" \
+           "    print(lib.gdn_attn_decode_workspace_size(ctypes.byref(a)), lib.gdn_attn_decode(ctypes.byref(a), None), flush=True)"
+    got = _alone(code % sizes)
+    assert got[::2] == [0] * len(sizes) and set(got[1::2]) <= {2, 5}
