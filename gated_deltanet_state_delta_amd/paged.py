@@ -172,7 +172,8 @@ def attn_decode_args(q, k_cache, v_cache, page_table, lens, *, scale=None, k_sca
         raise ValueError("out must be contiguous, 16-byte aligned, with q's shape and dtype")
     if lse is not None and (lse.shape != (B, T, hq) or lse.dtype != torch.float32 or not lse.is_contiguous()):
         raise ValueError("lse must be contiguous float32 [B, T, hq]")
-    qs = q.stride()
+    # a contiguous tensor's dimensions of one entry may carry any stride
+    qs = (T * hq * d, hq * d, d) if q.is_contiguous() else q.stride()
     a = _lib.AttnDecodeArgs(
         B, T, hq, hkv, d, _IO[dtype], cache_dtype, d ** -0.5 if scale is None else float(scale),
         q.data_ptr(), qs[0], qs[1], qs[2], k_cache.data_ptr(), *ks, v_cache.data_ptr(), *vs,

@@ -313,3 +313,28 @@ def test_workspace_size_of_refused_sizes_is_zero():
            "    print(lib.gdn_attn_decode_workspace_size(ctypes.byref(a)), lib.gdn_attn_decode(ctypes.byref(a), None), flush=True)"
     got = _alone(code % sizes)
     assert got[::2] == [0] * len(sizes) and set(got[1::2]) <= {2, 5}
+
+
+def test_attn_decode_args_read_queries_where_they_are():
+    """A contiguous query is read with its dense strides, whatever its
+    dimensions of one entry carry; others with their own."""
+    lone, step = torch.zeros(1, 1, 4, 64), torch.zeros(3, 2, 4, 64)[1:2].transpose(0, 1)
+    cases = [(_with_strides(lone, 7, 7, None, None), (256, 256, 64)), (step, (256, 256, 64)),
+             (_with_strides(torch.zeros(2, 1, 1, 64), None, 7, 13, None), (64, 64, 64)),
+             (torch.zeros(1, 2, 4, 64).transpose(1, 2).contiguous().transpose(1, 2), (512, 64, 128)),
+             (_with_strides(torch.zeros(1, 5, 4, 64), 3, None, None, None), (1280, 256, 64)),
+             (torch.zeros(1, 1, 9, 64)[:, :, 2:6], (256, 256, 64))]
+    for q, want in cases:
+        x = _inputs(q=q, page_table=torch.zeros(q.shape[0], 5, dtype=torch.int32), lens=torch.zeros(q.shape[0], dtype=torch.int32))
+        if q.shape[2] == 1:
+            x.update(k_cache=torch.zeros(3, 16, 1, 64), v_cache=torch.zeros(3, 16, 1, 64))
+        a, keep, out = gdn.attn_decode_args(**x)
+        got = (a.q_stride_row, a.q_stride_token, a.q_stride_head)
+        assert a.q == q.data_ptr() and out.shape == q.shape and out.is_contiguous()
+        # strides of dimensions of one entry are not used, but the library checks them
+        assert all(s % 8 == 0 for s in got) and all(s == w for s, w, n in zip(got, want, q.shape) if n > 1)
+        # the library takes them: the workspace, checked last, is what it refuses
+        a.k_cache, a.v_cache, a.q, a.out, a.page_table, a.lens = (FAKE * 2, FAKE * 4, FAKE * 32, FAKE * 64, FAKE * 96, FAKE * 97)
+        a.workspace, a.workspace_bytes = FAKE + 16, 1 << 20
+        assert L.load().gdn_attn_decode(ctypes.byref(a), None) == 4
+        assert b"workspace must be" in L.load().gdn_last_error()
