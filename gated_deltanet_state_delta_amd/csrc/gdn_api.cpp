@@ -330,11 +330,12 @@ static gdn_status cache_check(const char* f, int32_t batch, int32_t hkv, int32_t
 // order of tokens and heads inside a page, nothing smaller than dense.
 static gdn_status cache_layout(const char* f, const void* base, int64_t page, int64_t token, int64_t head,
                                int32_t page_size, int32_t hkv, int32_t d, size_t es) {
-  const int64_t unit = 16 / (int64_t)es, lim = int64_t(1) << 23;
+  // the kernels' offsets inside a page are 32 bits over 16 tokens, 64 bits over heads and pages
+  const int64_t unit = 16 / (int64_t)es, token_lim = int64_t(1) << 23, head_lim = int64_t(1) << 40;
   if (!aligned(base, 16) || page < 0 || page % unit != 0 || token % unit != 0 || head % unit != 0)
     return fail(GDN_ERR_LAYOUT, "%s: caches and their strides must be 16-byte aligned", f);
-  if (token < d || head < d || token >= lim || head >= lim)
-    return fail(GDN_ERR_LAYOUT, "%s: cache token and head strides must be in [d, 2^23)", f);
+  if (token < d || head < d || token >= token_lim || head >= head_lim)
+    return fail(GDN_ERR_LAYOUT, "%s: cache token strides must be in [d, 2^23), head strides must be in [d, 2^40)", f);
   // one of the two orders must keep every row apart
   if (token < (int64_t)(hkv - 1) * head + d && head < (int64_t)(page_size - 1) * token + d)
     return fail(GDN_ERR_LAYOUT, "%s: cache rows overlap", f);

@@ -92,7 +92,7 @@ def _cache_strides(c, shape, name):
     if heads == 1:
         sh = d
     if page == 1:
-        st = (heads - 1) * sh + d
+        st = d
     if n == 1:
         sp = (page - 1) * st + (heads - 1) * sh + d
         sp += -sp % 16

@@ -430,9 +430,9 @@ gdn_status gdn_conv1d(const gdn_conv1d_args* args, void* stream);
  * Common requirements: page_size and max_pages * page_size at most 2^30; d in
  * {32, 64, 128, 256}; hq a multiple of hkv (query head h reads key-value head
  * h*hkv/hq); a cache has io_dtype's type or GDN_E4M3; caches, q, k, v and out
- * 16-byte aligned, their strides non-negative multiples of 16 bytes; a cache's token
- * and head strides in [d, 2^23) elements, its rows apart and its page stride
- * not smaller than a page.
+ * 16-byte aligned, their strides non-negative multiples of 16 bytes; a cache's
+ * token strides in [d, 2^23) and its head strides in [d, 2^40) elements, its rows
+ * apart and its page stride not smaller than a page.
  * ========================================================================= */
 
 /* ----------------------------------------------------------------------------

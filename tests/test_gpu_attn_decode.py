@@ -479,3 +479,27 @@ def test_keys_of_nan_and_scores_of_minus_infinity(io, cache, T, page):
     assert out[1].isnan().all() and lse[1].isnan().all()
     assert (out[2] == 0).all() and (lse[2] == -float("inf")).all()
     assert out[3].isnan().all() and lse[3].isnan().all()
+
+
+@pytest.mark.parametrize("page", [65536, 65536 + 3])
+def test_heads_far_apart(page):
+    """Heads-first pages so long that a head begins 2^23 elements behind the
+    one before it: appended to and attended over."""
+    hkv, d, lens = 3, 128, torch.tensor([200, 33], dtype=torch.int32)
+    kc, vc = (torch.zeros(3, hkv, page, d, dtype=torch.bfloat16, device="cuda").transpose(1, 2) for _ in range(2))
+    assert kc.stride(2) >= 1 << 23
+    table = torch.tensor([[2], [0]], dtype=torch.int32)
+    g = torch.Generator().manual_seed(3)
+    k, v = (torch.randn(233, hkv, d, generator=g).bfloat16() for _ in range(2))
+    cu = torch.tensor([0, 200, 233], dtype=torch.int32)
+    gdn.kv_append(k.cuda(), v.cuda(), kc, vc, table.cuda(), lens.cuda(), cu_seqlens=cu.cuda())
+    for c, x in ((kc, k), (vc, v)):
+        assert torch.equal(c[2, :200].cpu(), x[:200]) and torch.equal(c[0, :33].cpu(), x[200:])
+        assert not c[1].any() and not c[2, 200:].any() and not c[0, 33:].any()
+    q = torch.randn(2, 1, 6, d, generator=g).bfloat16()
+    small = [torch.zeros(3, 256, hkv, d).bfloat16() for _ in range(2)]
+    for c, x in zip(small, (k, v)):
+        c[2, :200], c[0, :33] = x[:200], x[200:]
+    want = attn_ref(q, *small, table, lens, d ** -0.5)
+    out = gdn.attn_decode(q.cuda(), kc, vc, table.cuda(), lens.cuda())
+    assert ((out.double().cpu() - want[0]).abs() <= attn_bound(want[0], want[2], want[3], lens, d, "bf16")).all()

@@ -338,3 +338,23 @@ def test_attn_decode_args_read_queries_where_they_are():
         a.workspace, a.workspace_bytes = FAKE + 16, 1 << 20
         assert L.load().gdn_attn_decode(ctypes.byref(a), None) == 4
         assert b"workspace must be" in L.load().gdn_last_error()
+
+
+def test_head_strides_have_room():
+    """Only token strides have to stay below 2^23 elements: a heads-first page
+    of 65536 tokens with heads of 128 steps 2^23 elements from head to head.
+    The value cache, whose rows overlap, is what is refused."""
+    lib = L.load()
+    for head in (1 << 23, 1 << 33, (1 << 40) - 64):
+        cache = dict(d=64, n_pages=2, page_size=16)
+        attn = _attn(k_stride_token=64, k_stride_head=head, k_stride_page=2 * head, v_stride_token=64, v_stride_head=128, **cache)
+        append = _append(kc_stride_token=64, kc_stride_head=head, kc_stride_page=2 * head, vc_stride_token=64, vc_stride_head=128, **cache)
+        for f, a in ((lib.gdn_attn_decode, attn), (lib.gdn_kv_append, append)):
+            assert f(ctypes.byref(a), None) == 4 and b"rows overlap" in lib.gdn_last_error(), lib.gdn_last_error()
+    for over in (dict(k_stride_head=1 << 40, k_stride_page=1 << 42), dict(k_stride_head=(1 << 63) - 64, k_stride_page=(1 << 63) - 64)):
+        assert lib.gdn_attn_decode(ctypes.byref(_attn(k_stride_token=64, **over)), None) == 4
+        assert b"strides must be" in lib.gdn_last_error()
+    one = torch.empty_strided((4, 1, 3, 64), (1 << 25, 1, 1 << 23, 1), device="meta")  # pages of one token
+    x = _inputs(q=torch.zeros(2, 1, 3, 64), k_cache=one, v_cache=one)
+    a, keep, _ = gdn.attn_decode_args(**x)
+    assert (a.k_stride_page, a.k_stride_head) == (1 << 25, 1 << 23) and a.k_stride_token < 1 << 23
