@@ -103,7 +103,9 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendParams p) {
       back = p.T - i % p.T;
     } else {
       // the last row that starts at or before token i (offsets clamped to
-      // [0, total]); a token past that row's end belongs to none
+      // [0, total]); a token past that row's end belongs to none.  Offsets that
+      // decrease mislead the search, and the check of the range then leaves the
+      // token out.
       int lo = 0, hi = p.batch;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;

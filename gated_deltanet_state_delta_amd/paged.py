@@ -285,8 +285,8 @@ def kv_append(k, v, k_cache, v_cache, page_table, lens, *, cu_seqlens=None, k_sc
     """Write new tokens' keys and values into their pages (the caches are
     updated in place).
 
-    k, v: [B, T, hkv, d], T new tokens for every row, or with cu_seqlens
-    [B + 1] packed [tokens, hkv, d].  lens [B] counts the new tokens already:
+    k, v: [B, T, hkv, d], T new tokens for every row, or with non-decreasing
+    cu_seqlens [B + 1] packed [tokens, hkv, d].  lens [B] counts the new tokens already:
     row b's n tokens go to positions lens[b] - n .. lens[b] - 1 of its pages;
     tokens whose position lies outside the table or whose table entry is
     outside the cache are not written.  Caches, page_table and scales as for

@@ -501,10 +501,12 @@ gdn_status gdn_attn_decode(const gdn_attn_decode_args* args, void* stream);
  * to +-448 (NaN stays NaN); others store x as it is.
  *
  *   k, v  [total_tokens, hkv, d] io_dtype, strides {token, head}
- *   cu_seqlens  [batch + 1] int32: row b's tokens are cu_seqlens[b] ..
- *         cu_seqlens[b+1] - 1 (clamped to [0, total_tokens], a decreasing pair
- *         is empty, tokens of no row are not written), or NULL: total_tokens /
- *         batch tokens each (a whole number)
+ *   cu_seqlens  [batch + 1] int32, non-decreasing: row b's tokens are
+ *         cu_seqlens[b] .. cu_seqlens[b+1] - 1, offsets clamped to [0,
+ *         total_tokens]; tokens of no row are not written.  NULL: total_tokens /
+ *         batch tokens each (a whole number).  Where offsets decrease, tokens
+ *         may be left out; none goes anywhere but to its place in a row whose
+ *         range holds it
  * Rows whose new tokens fall into one page slot race (rows share full pages
  * only: see gdn_pages_fork).  total_tokens is at most 2^28.  batch == 0 or
  * total_tokens == 0 is a no-op.

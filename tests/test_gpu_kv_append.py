@@ -176,3 +176,28 @@ def test_steps_of_a_sequence_first_buffer(io, cache, rows, hkv):
         got = gdn.kv_append(*step, kc.cuda(), vc.cuda(), table.cuda(), lens.cuda(), k_scale=sd, v_scale=sd)
         for a, b in zip(got, want):
             assert torch.equal(_bits(a), b)
+
+
+@pytest.mark.parametrize("cu", [[5, 10, 0, 3], [0, 10, 5, 20], [20, 15, 10, 0], [0, 20, 20, 7, 7, 30, -4, 12], [9, 9, 2, 18, 1, 4]])
+def test_offsets_that_decrease_write_nothing_astray(cu):
+    """Tokens may be left out, but each that is written lies where its row has
+    it, and no other slot changes."""
+    rows, total, page = len(cu) - 1, 20, 8
+    lens = [20 - 3 * (b % 3) for b in range(rows)]
+    table, n_pages = paged(lens, page, seed=7)
+    kc, vc = caches(n_pages, page, 2, 32, "f32", 3)
+    k, v = (torch.randn(total, 2, 32, generator=torch.Generator().manual_seed(i)) for i in range(2))
+    got = gdn.kv_append(k.cuda(), v.cuda(), kc.cuda(), vc.cuda(), table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
+                        cu_seqlens=torch.tensor(cu, dtype=torch.int32).cuda())
+    at = [min(max(x, 0), total) for x in cu]
+    for old, x, new in ((kc, k, got[0].cpu()), (vc, v, got[1].cpu())):
+        for b in range(rows):
+            n = max(0, at[b + 1] - at[b])
+            for i in range(n):
+                pos = lens[b] - n + i
+                if pos < 0:
+                    continue
+                slot = new[int(table[b, pos // page]), pos % page]
+                if torch.equal(slot, x[at[b] + i]):
+                    slot.copy_(old[int(table[b, pos // page]), pos % page])
+        assert torch.equal(new, old)
