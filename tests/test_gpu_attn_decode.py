@@ -503,3 +503,31 @@ def test_heads_far_apart(page):
     want = attn_ref(q, *small, table, lens, d ** -0.5)
     out = gdn.attn_decode(q.cuda(), kc, vc, table.cuda(), lens.cuda())
     assert ((out.double().cpu() - want[0]).abs() <= attn_bound(want[0], want[2], want[3], lens, d, "bf16")).all()
+
+
+@pytest.mark.parametrize("page", [16, 5])
+@pytest.mark.parametrize("T,group", [(3, 4), (3, 8), (5, 9)])
+@pytest.mark.parametrize("d", [32, 64, 128, 256])
+@pytest.mark.parametrize("io,cache", [("bf16", "bf16"), ("f32", "f32"), ("bf16", "e4m3"), ("f32", "e4m3")])
+def test_several_new_tokens_of_every_type_and_head_size(io, cache, d, T, group, page):
+    """12, 24 and 45 query rows of a key-value head: the walks of one row tile,
+    of two and of more, each over pages that tiles do and do not divide.  Rows
+    shorter than the new tokens, an empty one, one of several tiles; unheld
+    slots are NaN, and so is the newest token's value in the longest row, which
+    the tokens before it do not see."""
+    lens = torch.tensor([T + 1, 0, 2, 30, 210], dtype=torch.int32)
+    table, n_pages = paged(lens, page, seed=T)
+    kc, vc = caches(n_pages, page, 2, d, cache, seed=T * 100 + d)
+    kc, vc = (poison_unheld(c, table, lens, page, float("nan")) for c in (kc, vc))
+    ks, vs = _scales(cache, 2)
+    q = torch.randn(5, T, 2 * group, d, generator=torch.Generator().manual_seed(d + T)).to(DT[io])
+    ref = attn_ref(q, kc, vc, table, lens, d ** -0.5, ks, vs)
+    _check(q, kc, vc, table, lens, io, ks, vs, ref=ref)
+    w = vc.float()
+    w[int(table[4, 209 // page]), 209 % page] = float("nan")
+    out = gdn.attn_decode(q.cuda(), kc.cuda(), w.to(vc.dtype).cuda(), table.cuda(), lens.cuda(), k_scale=_dev(ks),
+                          v_scale=_dev(vs)).double().cpu()
+    assert out[4, -1].isnan().all()
+    keep = torch.ones(5, T, dtype=torch.bool)
+    keep[4, -1] = False
+    assert ((out - ref[0]).abs() <= attn_bound(ref[0], ref[2], ref[3], lens, d, io))[keep].all()
