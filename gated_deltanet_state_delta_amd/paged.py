@@ -357,6 +357,8 @@ def pages_args(page_table, lens, refs, page_size, out=None, apart=False, workspa
         raise ValueError("page_table must be [rows, max_pages]")
     if refs.dim() != 1 or refs.shape[0] < 1:
         raise ValueError("refs must be [n_pages]")
+    if int(page_size) != page_size or not _I32_MIN <= page_size <= _I32_MAX:
+        raise ValueError("page_size must be a whole number of 32 bits, got %s" % (page_size,))
     rows, n = shape[0], refs.shape[0]
     table, table_stride, width = _table(page_table, rows)
     refs_in = _i32(refs, "refs", (n,))

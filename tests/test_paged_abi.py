@@ -358,3 +358,13 @@ def test_head_strides_have_room():
     x = _inputs(q=torch.zeros(2, 1, 3, 64), k_cache=one, v_cache=one)
     a, keep, _ = gdn.attn_decode_args(**x)
     assert (a.k_stride_page, a.k_stride_head) == (1 << 25, 1 << 23) and a.k_stride_token < 1 << 23
+
+
+def test_page_sizes_that_no_int32_holds_are_refused():
+    """They would reach the library as other numbers."""
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    for page_size in ((1 << 32) + 16, -(1 << 32) + 16, 1 << 31, 16.5):
+        with pytest.raises(ValueError):
+            gdn.pages_args(i32(4, 5), i32(4), i32(9), page_size)
+    a, keep, _ = gdn.pages_args(i32(4, 5), i32(4), i32(9), torch.tensor(16))
+    assert a.page_size == 16
