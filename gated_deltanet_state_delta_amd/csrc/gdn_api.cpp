@@ -353,7 +353,9 @@ static gdn_status attn_sizes(const char* f, const gdn_attn_decode_args& a) {
   // Each size is below 2^31 and hq at most 2^16: in this order no product overflows 64 bits.
   if ((int64_t)a.batch * a.hq >= (int64_t(1) << 31) || (int64_t)a.batch * a.hq * a.T >= (int64_t(1) << 31))
     return fail(GDN_ERR_UNSUPPORTED, "%s: batch * hq * T must be below 2^31", f);
-  // one workgroup per row, key-value head and 16 query rows; a grid has at most 2^24 of 256 threads
+  // A wave takes 16 query rows or more of a row and key-value head, or a share of several rows; a workgroup's four
+  // waves hold row tiles padded to less than twice their number.  So fewer than 2^22 workgroups (and 8 for the last
+  // of the 8 XCDs), where a grid ends at 2^24 of 256 threads.
   if ((int64_t)a.batch * a.hkv * (((int64_t)a.T * (a.hq / a.hkv) + 15) / 16) > (int64_t(1) << 23))
     return fail(GDN_ERR_UNSUPPORTED, "%s: batch * hkv * ceil(T * hq / hkv / 16) must be at most 2^23", f);
   // the rows' tiles of 16 keys and more are counted in 32 bits

@@ -11,7 +11,7 @@
 // T * hq/hkv query rows of its head only, so the cache's bytes over the HBM
 // rate are the floor; the products run on MFMA mostly to keep the VALU free.
 //
-// Work split: a wave walks keys of one key-value head for 16 query rows, by
+// Work split: a wave walks keys of one key-value head for 16 or 32 query rows, by
 // itself: no barrier, and no LDS where pages are whole subtiles.  The lengths
 // are known on the device only, so the keys of all rows, laid end to end in
 // steps of one tile, are dealt out evenly: each of a fixed number of waves (as

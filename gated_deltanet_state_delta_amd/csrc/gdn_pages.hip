@@ -25,7 +25,7 @@ typedef u32x4 u32x4_any __attribute__((aligned(1)));
 
 constexpr int kCopyChunk = 16384;  // bytes of a page that one workgroup copies at a time
 
-// HBM-bound for large pages: 256 slots of 2 MiB take 191 us (5.6 TB/s read
+// HBM-bound for large pages: 256 slots of 2 MiB take 188 us (5.7 TB/s read
 // and written; 205 us with ordinary loads and stores, which leave the copy in
 // the caches, and 206 with chunks of 128 KiB).  Pieces of 16 bytes, four loads in
 // flight per thread; the last bytes of a page one by one.  Workgroups step
