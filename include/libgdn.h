@@ -447,8 +447,8 @@ gdn_status gdn_conv1d(const gdn_conv1d_args* args, void* stream);
  * invalid pages), or whose scores are all -inf, gets zeros and lse -inf.  A NaN
  * in a token's query or in a key that it sees makes its result and lse NaN.
  * Values at positions that a token does not see never reach its result,
- * infinities and NaN included.  Sums and
- * the softmax are fp32; bf16 weights enter the product as two bf16 terms.
+ * infinities and NaN included.  Sums and the softmax are fp32; bf16 weights
+ * enter the product as two bf16 terms.
  *
  *   q    [batch, T, hq, d] io_dtype, strides {row, token, head}
  *   out  [batch, T, hq, d] io_dtype, dense
@@ -463,8 +463,9 @@ gdn_status gdn_conv1d(const gdn_conv1d_args* args, void* stream);
  * 0 when none is of use) the rows' keys are dealt evenly to the waves of one
  * launch and the parts of a row joined by a second; with less, one wave walks
  * each row and key-value head: the same result up to rounding order.  The size
- * depends on sizes alone, not on lens, and is 0 for sizes that the call refuses.  The library keeps nothing in the
- * workspace between calls; calls that share one must not overlap.
+ * depends on sizes alone, not on lens, and is 0 for sizes that the call refuses.
+ * The library keeps nothing in the workspace between calls; calls that share one
+ * must not overlap.
  * ------------------------------------------------------------------------- */
 typedef struct {
   int32_t batch, T, hq, hkv, d;
