@@ -17,7 +17,13 @@ and, for the softmax-attention layers beside them (paged.py):
 
   attn_decode(q, k_cache, v_cache, page_table, lens, ...) -> out | (out, lse)
   kv_append(k, v, k_cache, v_cache, page_table, lens, ...) -> (k_cache, v_cache)
+  kv_read(k_cache, v_cache, page_table, lens, tokens, ...) -> (k, v)
   pages_copy, pages_extend, pages_fork, pages_free, pages_compact
+
+with the rotary positions of their queries and keys (rope.py):
+
+  rope(q, k, inv_freq, lens=... | positions=..., ...) -> (q, k)
+  rope_frequencies(rot, ...) -> (inv_freq, factor)
 """
 from __future__ import annotations
 
@@ -29,13 +35,15 @@ import torch
 from . import _lib
 from ._lib import GdnError
 from .paged import (attn_decode, attn_decode_args, attn_decode_workspace_size, kv_append, kv_append_args,
-                    pages_args, pages_compact, pages_copy, pages_extend, pages_fork, pages_free)
+                    kv_read, kv_read_args, pages_args, pages_compact, pages_copy, pages_extend, pages_fork, pages_free)
+from .rope import rope, rope_args, rope_frequencies
 
 __all__ = ["gate", "prefill", "decode", "conv1d", "state_update", "version", "GdnError",
            "prefill_args", "decode_args", "conv1d_args", "prefill_workspace_size",
            "prefill_noalloc", "wait_timeouts", "attn_decode", "attn_decode_args",
            "attn_decode_workspace_size", "kv_append", "kv_append_args", "pages_copy", "pages_args",
-           "pages_extend", "pages_fork", "pages_free", "pages_compact"]
+           "pages_extend", "pages_fork", "pages_free", "pages_compact", "kv_read", "kv_read_args", "rope",
+           "rope_args", "rope_frequencies"]
 
 _DT = {torch.float32: _lib.GDN_F32, torch.bfloat16: _lib.GDN_BF16}
 # update_rule of the ONNX card -> gdn_update_rule

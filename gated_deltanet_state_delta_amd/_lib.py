@@ -13,7 +13,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libgdn.so")
 
 GDN_OK = 0
-GDN_F32, GDN_BF16, GDN_E4M3 = 0, 1, 2
+GDN_F32, GDN_BF16, GDN_E4M3, GDN_I8 = 0, 1, 2, 3
 GDN_DECAY_LOG, GDN_DECAY_GAMMA = 0, 1
 
 STATUS_NAMES = {0: "GDN_OK", 1: "GDN_ERR_NULL", 2: "GDN_ERR_SHAPE", 3: "GDN_ERR_DTYPE",
@@ -22,7 +22,8 @@ STATUS_NAMES = {0: "GDN_OK", 1: "GDN_ERR_NULL", 2: "GDN_ERR_SHAPE", 3: "GDN_ERR_
 # every extern "C" symbol include/libgdn.h declares
 EXPORTED = ("gdn_last_error", "gdn_version", "gdn_gate", "gdn_prefill", "gdn_prefill_workspace_size",
             "gdn_prefill_noalloc", "gdn_decode", "gdn_conv1d", "gdn_wait_timeouts",
-            "gdn_attn_decode", "gdn_attn_decode_workspace_size", "gdn_kv_append", "gdn_pages_copy",
+            "gdn_attn_decode", "gdn_attn_decode_workspace_size", "gdn_kv_append", "gdn_kv_read", "gdn_rope",
+            "gdn_pages_copy",
             "gdn_pages_workspace_size", "gdn_pages_extend", "gdn_pages_fork", "gdn_pages_free",
             "gdn_pages_compact")
 NOALLOC_SCRATCH_BYTES = 32 << 20  # GDN_NOALLOC_SCRATCH_BYTES
@@ -90,6 +91,7 @@ class AttnDecodeArgs(ctypes.Structure):
         ("page_table", _vp), ("page_table_stride", _i64), ("lens", _vp),
         ("k_scale", _vp), ("v_scale", _vp),
         ("out", _vp), ("lse", _vp), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t),
+        ("scale_block", _i32), ("k_block_scale", _vp), ("v_block_scale", _vp),
     ]
 
 
@@ -105,6 +107,24 @@ class KvAppendArgs(ctypes.Structure):
         ("n_pages", _i32), ("page_size", _i32), ("max_pages", _i32),
         ("page_table", _vp), ("page_table_stride", _i64), ("lens", _vp),
         ("k_scale", _vp), ("v_scale", _vp),
+        ("scale_block", _i32), ("k_block_scale", _vp), ("v_block_scale", _vp),
+    ]
+
+
+class KvReadArgs(ctypes.Structure):
+    _fields_ = KvAppendArgs._fields_ + [("zero_rest", _i32)]
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = [
+        ("total_tokens", _i64), ("batch", _i32), ("hq", _i32), ("hkv", _i32), ("d", _i32), ("rot", _i32),
+        ("io_dtype", _i32), ("interleaved", _i32), ("factor", _f32),
+        ("q", _vp), ("q_stride_token", _i64), ("q_stride_head", _i64),
+        ("k", _vp), ("k_stride_token", _i64), ("k_stride_head", _i64),
+        ("q_out", _vp), ("qo_stride_token", _i64), ("qo_stride_head", _i64),
+        ("k_out", _vp), ("ko_stride_token", _i64), ("ko_stride_head", _i64),
+        ("inv_freq", _vp), ("positions", _vp), ("positions_i64", _i32),
+        ("lens", _vp), ("cu_seqlens", _vp), ("zero_rest", _i32),
     ]
 
 
@@ -156,6 +176,10 @@ def load(path: str | None = None):
         lib.gdn_attn_decode.argtypes = [ctypes.POINTER(AttnDecodeArgs), _vp]
         lib.gdn_kv_append.restype = ctypes.c_int
         lib.gdn_kv_append.argtypes = [ctypes.POINTER(KvAppendArgs), _vp]
+        lib.gdn_kv_read.restype = ctypes.c_int
+        lib.gdn_kv_read.argtypes = [ctypes.POINTER(KvReadArgs), _vp]
+        lib.gdn_rope.restype = ctypes.c_int
+        lib.gdn_rope.argtypes = [ctypes.POINTER(RopeArgs), _vp]
         lib.gdn_pages_copy.restype = ctypes.c_int
         lib.gdn_pages_copy.argtypes = [_vp, _i64, _i64, _i32, _vp, _vp, _i64, _vp]
         lib.gdn_pages_workspace_size.restype = ctypes.c_size_t

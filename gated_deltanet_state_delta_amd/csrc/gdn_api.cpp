@@ -62,6 +62,7 @@ hipError_t noalloc_scratch(void** out) {
 bool head_size_ok(int32_t d) { return d == 16 || d == 32 || d == 64 || d == 128; }
 bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p % n) == 0; }
 size_t elem_size(int32_t dt) { return dt == GDN_BF16 ? 2 : 4; }
+size_t cache_elem(int32_t dt) { return dt == GDN_E4M3 || dt == GDN_I8 ? 1 : elem_size(dt); }
 
 }  // namespace
 
@@ -299,8 +300,8 @@ gdn_status gdn_conv1d(const gdn_conv1d_args* p, void* stream) {
 static gdn_status cache_sizes(const char* f, int32_t batch, int32_t hkv, int32_t d, int32_t io_dtype,
                               int32_t cache_dtype, int32_t n_pages, int32_t page_size, int32_t max_pages) {
   if (io_dtype != GDN_F32 && io_dtype != GDN_BF16) return fail(GDN_ERR_DTYPE, "%s: io_dtype %d", f, io_dtype);
-  if (cache_dtype != io_dtype && cache_dtype != GDN_E4M3)
-    return fail(GDN_ERR_DTYPE, "%s: cache_dtype %d (io_dtype's type or GDN_E4M3)", f, cache_dtype);
+  if (cache_dtype != io_dtype && cache_dtype != GDN_E4M3 && cache_dtype != GDN_I8)
+    return fail(GDN_ERR_DTYPE, "%s: cache_dtype %d (io_dtype's type, GDN_E4M3 or GDN_I8)", f, cache_dtype);
   if (batch < 0 || hkv <= 0 || d <= 0 || n_pages < 0 || page_size <= 0 || max_pages < 0)
     return fail(GDN_ERR_SHAPE, "%s: bad sizes batch=%d hkv=%d d=%d n_pages=%d page_size=%d max_pages=%d", f, batch,
                 hkv, d, n_pages, page_size, max_pages);
@@ -312,18 +313,38 @@ static gdn_status cache_sizes(const char* f, int32_t batch, int32_t hkv, int32_t
   return GDN_OK;
 }
 
-// The same with the page table's stride and the scales.
-static gdn_status cache_check(const char* f, int32_t batch, int32_t hkv, int32_t d, int32_t io_dtype,
-                              int32_t cache_dtype, int32_t n_pages, int32_t page_size, int32_t max_pages,
-                              int64_t table_stride, const float* k_scale, const float* v_scale) {
-  const gdn_status st = cache_sizes(f, batch, hkv, d, io_dtype, cache_dtype, n_pages, page_size, max_pages);
-  if (st != GDN_OK) return st;
-  if (table_stride < max_pages) return fail(GDN_ERR_LAYOUT, "%s: page_table_stride smaller than max_pages", f);
-  if (cache_dtype == GDN_E4M3 && (!k_scale || !v_scale))
-    return fail(GDN_ERR_NULL, "%s: an e4m3 cache needs k_scale and v_scale", f);
-  if (cache_dtype != GDN_E4M3 && (k_scale || v_scale))
-    return fail(GDN_ERR_SHAPE, "%s: k_scale and v_scale are for e4m3 caches", f);
+// The scales of a cache: a factor a head, or block scales.
+static gdn_status scales_check(const char* f, int32_t cache_dtype, int32_t n_pages, int32_t page_size, const float* k_scale,
+                               const float* v_scale, int32_t block, const float* k_blocks, const float* v_blocks) {
+  if (block < 0) return fail(GDN_ERR_SHAPE, "%s: scale_block=%d", f, block);
+  if (block == 0) {
+    if (k_blocks || v_blocks) return fail(GDN_ERR_SHAPE, "%s: block scales need scale_block", f);
+    if (cache_dtype == GDN_I8) return fail(GDN_ERR_NULL, "%s: an int8 cache needs block scales", f);
+    if (cache_dtype == GDN_E4M3 && (!k_scale || !v_scale))
+      return fail(GDN_ERR_NULL, "%s: an e4m3 cache needs k_scale and v_scale", f);
+    if (cache_dtype != GDN_E4M3 && (k_scale || v_scale))
+      return fail(GDN_ERR_SHAPE, "%s: k_scale and v_scale are for e4m3 caches", f);
+    return GDN_OK;
+  }
+  if (cache_dtype != GDN_E4M3 && cache_dtype != GDN_I8)
+    return fail(GDN_ERR_SHAPE, "%s: block scales are for 8-bit caches", f);
+  if (k_scale || v_scale) return fail(GDN_ERR_SHAPE, "%s: k_scale and v_scale with block scales", f);
+  if (block > page_size || page_size % block != 0)
+    return fail(GDN_ERR_SHAPE, "%s: scale_block=%d does not divide page_size=%d", f, block, page_size);
+  if (block > 65536) return fail(GDN_ERR_UNSUPPORTED, "%s: scale_block=%d (supported up to 65536)", f, block);
+  if (n_pages > 0 && (!k_blocks || !v_blocks)) return fail(GDN_ERR_NULL, "%s: k_block_scale and v_block_scale are required", f);
+  if (!aligned(k_blocks, 4) || !aligned(v_blocks, 4))
+    return fail(GDN_ERR_LAYOUT, "%s: block scales must be 4-byte aligned", f);
   return GDN_OK;
+}
+
+// What the calls over a paged cache share with its page table and scales (A: one of their argument structs).
+extern "C++" template <typename A>
+static gdn_status cache_check(const char* f, const A& a) {
+  const gdn_status st = cache_sizes(f, a.batch, a.hkv, a.d, a.io_dtype, a.cache_dtype, a.n_pages, a.page_size, a.max_pages);
+  if (st != GDN_OK) return st;
+  if (a.page_table_stride < a.max_pages) return fail(GDN_ERR_LAYOUT, "%s: page_table_stride smaller than max_pages", f);
+  return scales_check(f, a.cache_dtype, a.n_pages, a.page_size, a.k_scale, a.v_scale, a.scale_block, a.k_block_scale, a.v_block_scale);
 }
 
 // Strides of a [page, token, head, d] cache (es bytes an element): either
@@ -381,14 +402,13 @@ gdn_status gdn_attn_decode(const gdn_attn_decode_args* p, void* stream) {
   g_err[0] = 0;
   if (!p) return fail(GDN_ERR_NULL, "%s: args is NULL", f);
   const gdn_attn_decode_args& a = *p;
-  gdn_status st = cache_check(f, a.batch, a.hkv, a.d, a.io_dtype, a.cache_dtype, a.n_pages, a.page_size, a.max_pages,
-                              a.page_table_stride, a.k_scale, a.v_scale);
+  gdn_status st = cache_check(f, a);
   if (st != GDN_OK) return st;
   st = attn_sizes(f, a);
   if (st != GDN_OK || a.batch == 0) return st;
   if (!a.q || !a.out || !a.lens || (a.max_pages > 0 && !a.page_table) || (a.n_pages > 0 && (!a.k_cache || !a.v_cache)))
     return fail(GDN_ERR_NULL, "%s: q, caches, page_table, lens and out are required", f);
-  const size_t es = elem_size(a.io_dtype), ce = a.cache_dtype == GDN_E4M3 ? 1 : es;
+  const size_t es = elem_size(a.io_dtype), ce = cache_elem(a.cache_dtype);
   if (!aligned(a.q, 16) || !aligned(a.out, 16)) return fail(GDN_ERR_LAYOUT, "%s: q and out must be 16-byte aligned", f);
   const int64_t unit = 16 / (int64_t)es;
   if (a.q_stride_row < 0 || a.q_stride_token < 0 || a.q_stride_head < 0 || a.q_stride_row % unit != 0 ||
@@ -410,35 +430,117 @@ gdn_status gdn_attn_decode(const gdn_attn_decode_args* p, void* stream) {
   return from_hip(gdn::launch_attn_decode(a, (hipStream_t)stream), "gdn_attn_decode launch");
 }
 
-gdn_status gdn_kv_append(const gdn_kv_append_args* p, void* stream) {
-  static const char* f = "gdn_kv_append";
-  g_err[0] = 0;
-  if (!p) return fail(GDN_ERR_NULL, "%s: args is NULL", f);
-  const gdn_kv_append_args& a = *p;
-  gdn_status st = cache_check(f, a.batch, a.hkv, a.d, a.io_dtype, a.cache_dtype, a.n_pages, a.page_size, a.max_pages,
-                              a.page_table_stride, a.k_scale, a.v_scale);
+// What gdn_kv_append and gdn_kv_read check alike.  done: there is nothing to do.
+extern "C++" template <typename A>
+static gdn_status tokens_check(const char* f, const A& a, bool& done) {
+  gdn_status st = cache_check(f, a);
   if (st != GDN_OK) return st;
   if (a.total_tokens < 0) return fail(GDN_ERR_SHAPE, "%s: total_tokens=%lld", f, (long long)a.total_tokens);
   if (a.hkv > 65536) return fail(GDN_ERR_UNSUPPORTED, "%s: hkv=%d (supported up to 65536)", f, a.hkv);
   if (a.total_tokens > (int64_t(1) << 28)) return fail(GDN_ERR_UNSUPPORTED, "%s: total_tokens must be at most 2^28", f);
-  if (a.batch == 0 || a.total_tokens == 0) return GDN_OK;
-  if (!a.cu_seqlens && a.total_tokens % a.batch != 0)
+  done = a.batch == 0 || a.total_tokens == 0;
+  if (!done && !a.cu_seqlens && a.total_tokens % a.batch != 0)
     return fail(GDN_ERR_SHAPE, "%s: without cu_seqlens total_tokens %lld must be a multiple of batch %d", f,
                 (long long)a.total_tokens, a.batch);
-  if (a.n_pages == 0 || a.max_pages == 0) return GDN_OK;  // no page to write to
-  if (!a.k || !a.v || !a.k_cache || !a.v_cache || !a.page_table || !a.lens)
-    return fail(GDN_ERR_NULL, "%s: k, v, caches, page_table and lens are required", f);
-  const size_t es = elem_size(a.io_dtype), ce = a.cache_dtype == GDN_E4M3 ? 1 : es;
+  return GDN_OK;
+}
+extern "C++" template <typename A>
+static gdn_status tokens_layout(const char* f, const A& a) {
+  const size_t es = elem_size(a.io_dtype), ce = cache_elem(a.cache_dtype);
   const int64_t unit = 16 / (int64_t)es;
   const int64_t strides[] = {a.k_stride_token, a.k_stride_head, a.v_stride_token, a.v_stride_head};
   if (!aligned(a.k, 16) || !aligned(a.v, 16)) return fail(GDN_ERR_LAYOUT, "%s: k and v must be 16-byte aligned", f);
   for (int64_t s : strides)
     if (s < 0 || s % unit != 0) return fail(GDN_ERR_LAYOUT, "%s: k and v strides must be non-negative multiples of 16 bytes", f);
-  st = cache_layout(f, a.k_cache, a.kc_stride_page, a.kc_stride_token, a.kc_stride_head, a.page_size, a.hkv, a.d, ce);
+  if (a.n_pages == 0) return GDN_OK;
+  const gdn_status st =
+      cache_layout(f, a.k_cache, a.kc_stride_page, a.kc_stride_token, a.kc_stride_head, a.page_size, a.hkv, a.d, ce);
   if (st != GDN_OK) return st;
-  st = cache_layout(f, a.v_cache, a.vc_stride_page, a.vc_stride_token, a.vc_stride_head, a.page_size, a.hkv, a.d, ce);
+  return cache_layout(f, a.v_cache, a.vc_stride_page, a.vc_stride_token, a.vc_stride_head, a.page_size, a.hkv, a.d, ce);
+}
+
+gdn_status gdn_kv_append(const gdn_kv_append_args* p, void* stream) {
+  static const char* f = "gdn_kv_append";
+  g_err[0] = 0;
+  if (!p) return fail(GDN_ERR_NULL, "%s: args is NULL", f);
+  const gdn_kv_append_args& a = *p;
+  bool done = false;
+  gdn_status st = tokens_check(f, a, done);
+  if (st != GDN_OK || done) return st;
+  if (a.n_pages == 0 || a.max_pages == 0) return GDN_OK;  // no page to write to
+  if (!a.k || !a.v || !a.k_cache || !a.v_cache || !a.page_table || !a.lens)
+    return fail(GDN_ERR_NULL, "%s: k, v, caches, page_table and lens are required", f);
+  st = tokens_layout(f, a);
   if (st != GDN_OK) return st;
-  return from_hip(gdn::launch_kv_append(a, (hipStream_t)stream), "gdn_kv_append launch");
+  if (a.scale_block == 0) return from_hip(gdn::launch_kv_append(a, (hipStream_t)stream), "gdn_kv_append launch");
+  // its blocks are counted in 32 bits, 64 to a workgroup
+  if (a.total_tokens / a.scale_block + 2 * (int64_t)a.batch >= (int64_t(1) << 29))
+    return fail(GDN_ERR_UNSUPPORTED, "%s: total_tokens / scale_block + 2 * batch must be below 2^29", f);
+  return from_hip(gdn::launch_kv_quantise(a, (hipStream_t)stream), "gdn_kv_append launch");
+}
+
+gdn_status gdn_kv_read(const gdn_kv_read_args* p, void* stream) {
+  static const char* f = "gdn_kv_read";
+  g_err[0] = 0;
+  if (!p) return fail(GDN_ERR_NULL, "%s: args is NULL", f);
+  const gdn_kv_read_args& a = *p;
+  bool done = false;
+  gdn_status st = tokens_check(f, a, done);
+  if (st != GDN_OK || done) return st;
+  if (!a.k || !a.v || !a.lens || (a.max_pages > 0 && !a.page_table) || (a.n_pages > 0 && (!a.k_cache || !a.v_cache)))
+    return fail(GDN_ERR_NULL, "%s: k, v, caches, page_table and lens are required", f);
+  st = tokens_layout(f, a);
+  if (st != GDN_OK) return st;
+  return from_hip(gdn::launch_kv_read(a, (hipStream_t)stream), "gdn_kv_read launch");
+}
+
+// One input and output of gdn_rope.
+static gdn_status rope_layout(const char* f, const char* name, const gdn_rope_args& a, int32_t heads, const void* in,
+                              int64_t st, int64_t sh, const void* out, int64_t ot, int64_t oh) {
+  const size_t es = elem_size(a.io_dtype);
+  if (!aligned(in, es) || !aligned(out, es)) return fail(GDN_ERR_LAYOUT, "%s: %s is not aligned to its elements", f, name);
+  const int64_t lim = int64_t(1) << 40;
+  if (st < 0 || sh < 0 || ot < 0 || oh < 0 || st >= lim || sh >= lim || ot >= lim || oh >= lim)
+    return fail(GDN_ERR_LAYOUT, "%s: strides of %s must be in [0, 2^40)", f, name);
+  if (in == out) {
+    if ((a.total_tokens > 1 && st != ot) || (heads > 1 && sh != oh))
+      return fail(GDN_ERR_LAYOUT, "%s: %s in place needs equal strides", f, name);
+    return GDN_OK;
+  }
+  auto span = [&](int64_t t, int64_t h) { return ((size_t)(a.total_tokens - 1) * t + (size_t)(heads - 1) * h + a.d) * es; };
+  const uintptr_t i0 = (uintptr_t)in, o0 = (uintptr_t)out;
+  if (i0 < o0 + span(ot, oh) && o0 < i0 + span(st, sh)) return fail(GDN_ERR_LAYOUT, "%s: the output of %s overlaps it", f, name);
+  return GDN_OK;
+}
+
+gdn_status gdn_rope(const gdn_rope_args* p, void* stream) {
+  static const char* f = "gdn_rope";
+  g_err[0] = 0;
+  if (!p) return fail(GDN_ERR_NULL, "%s: args is NULL", f);
+  const gdn_rope_args& a = *p;
+  if (a.io_dtype != GDN_F32 && a.io_dtype != GDN_BF16) return fail(GDN_ERR_DTYPE, "%s: io_dtype %d", f, a.io_dtype);
+  if (a.total_tokens < 0 || a.batch < 0 || a.hq <= 0 || a.hkv < 0 || a.d <= 0 || a.rot <= 0)
+    return fail(GDN_ERR_SHAPE, "%s: bad sizes total_tokens=%lld batch=%d hq=%d hkv=%d d=%d rot=%d", f,
+                (long long)a.total_tokens, a.batch, a.hq, a.hkv, a.d, a.rot);
+  if (a.rot % 2 != 0 || a.rot > a.d) return fail(GDN_ERR_SHAPE, "%s: rot=%d must be even and at most d=%d", f, a.rot, a.d);
+  if (a.d > 1024) return fail(GDN_ERR_UNSUPPORTED, "%s: d=%d (supported up to 1024)", f, a.d);
+  if ((int64_t)a.hq + a.hkv > 65536) return fail(GDN_ERR_UNSUPPORTED, "%s: hq + hkv must be at most 65536", f);
+  if (a.total_tokens > (1 << 24)) return fail(GDN_ERR_UNSUPPORTED, "%s: total_tokens must be at most 2^24", f);
+  if (a.total_tokens == 0 || (a.batch == 0 && !a.positions)) return GDN_OK;
+  if (!a.positions && !a.cu_seqlens && a.total_tokens % a.batch != 0)
+    return fail(GDN_ERR_SHAPE, "%s: without cu_seqlens total_tokens %lld must be a multiple of batch %d", f,
+                (long long)a.total_tokens, a.batch);
+  if (!a.q || !a.q_out || !a.inv_freq || (!a.positions && !a.lens))
+    return fail(GDN_ERR_NULL, "%s: q, q_out, inv_freq and positions or lens are required", f);
+  if ((a.hkv > 0) != (a.k != nullptr) || (a.k != nullptr) != (a.k_out != nullptr))
+    return fail(GDN_ERR_NULL, "%s: k, k_out and hkv go together", f);
+  if (!aligned(a.inv_freq, 8) || (a.positions && !aligned(a.positions, a.positions_i64 ? 8 : 4)))
+    return fail(GDN_ERR_LAYOUT, "%s: inv_freq and positions must be aligned to their elements", f);
+  gdn_status st = rope_layout(f, "q", a, a.hq, a.q, a.q_stride_token, a.q_stride_head, a.q_out, a.qo_stride_token, a.qo_stride_head);
+  if (st == GDN_OK && a.k)
+    st = rope_layout(f, "k", a, a.hkv, a.k, a.k_stride_token, a.k_stride_head, a.k_out, a.ko_stride_token, a.ko_stride_head);
+  if (st != GDN_OK) return st;
+  return from_hip(gdn::launch_rope(a, (hipStream_t)stream), "gdn_rope launch");
 }
 
 gdn_status gdn_pages_copy(void* pool, int64_t page_bytes, int64_t page_stride, int32_t n_pages, const int32_t* src,

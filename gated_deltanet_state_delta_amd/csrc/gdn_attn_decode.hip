@@ -108,13 +108,14 @@ static void launch_join(const AttnParams& p, int d, hipStream_t stream) {
 // tiles that fill the card by themselves, and batches of so many rows that
 // finding the shares would cost more than their evenness gives.
 constexpr int kMostRows = 4096;
+static int cache_bytes(int dtype) { return dtype == GDN_F32 ? 4 : dtype == GDN_BF16 ? 2 : 1; }
 // Row tiles (see attn_rows16) of a key-value head.
 static int attn_tiles(const gdn_attn_decode_args& a) {
   const int R = a.T * (a.hq / a.hkv), rows = 16 * attn_rows16(attn_kind(a.T, R), a.d, a.io_dtype == GDN_BF16 ? 2 : 4);
   return (R + rows - 1) / rows;
 }
 static int attn_shares(const gdn_attn_decode_args& a) {
-  const int es = a.cache_dtype == GDN_E4M3 ? 1 : a.io_dtype == GDN_BF16 ? 2 : 4, tile = attn_tile(es, a.d);
+  const int es = cache_bytes(a.cache_dtype), tile = attn_tile(es, a.d);
   const int64_t cap = (int64_t)a.max_pages * a.page_size, steps = a.batch * ((cap + tile - 1) / tile);
   const int alone = tile < 32 ? 64 : 128;
   if (cap <= alone || a.batch > kMostRows || (int64_t)a.batch * a.hq * a.T > (1 << 24)) return 0;
@@ -131,9 +132,18 @@ size_t attn_workspace_bytes(const gdn_attn_decode_args& a) {
   return (2 * (size_t)shares * a.hq * a.T * (a.d + 2) + 2 * (size_t)a.batch) * sizeof(float);
 }
 
+// j / n = (j * mul) >> shift for j < 2^31 and n up to 2^30: with s = ceil(log2(n)) and
+// mul = ceil(2^(31 + s) / n), the error of mul is below 2^s.
+static void divider(int n, uint32_t& mul, uint32_t& shift) {
+  int s = 0;
+  while ((1 << s) < n) ++s;
+  mul = (uint32_t)((((uint64_t)1 << (31 + s)) + n - 1) / n);
+  shift = 31 + s;
+}
+
 hipError_t launch_attn_decode(const gdn_attn_decode_args& a, hipStream_t stream) {
   const int io = a.io_dtype == GDN_BF16 ? 2 : 4;
-  const int ce = a.cache_dtype == GDN_E4M3 ? 1 : io;
+  const int ce = cache_bytes(a.cache_dtype);
   AttnParams p;
   p.q = a.q;
   p.q_sb = a.q_stride_row * io;
@@ -154,6 +164,9 @@ hipError_t launch_attn_decode(const gdn_attn_decode_args& a, hipStream_t stream)
   p.lens = a.lens;
   p.k_scale = a.k_scale;
   p.v_scale = a.v_scale;
+  p.k_blocks = a.k_block_scale;
+  p.v_blocks = a.v_block_scale;
+  p.nblk = a.scale_block > 0 ? a.page_size / a.scale_block : 0;
   p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
   p.batch = a.batch;
   p.T = a.T;
@@ -165,12 +178,8 @@ hipError_t launch_attn_decode(const gdn_attn_decode_args& a, hipStream_t stream)
   p.n_pages = a.n_pages;
   p.page_size = a.page_size;
   p.cap = a.max_pages * a.page_size;
-  // j / page_size for j < 2^31 and page_size up to 2^30: with s = ceil(log2(page_size)) and
-  // mul = ceil(2^(31 + s) / page_size), the error of mul is below 2^s.
-  int s = 0;
-  while ((1 << s) < a.page_size) ++s;
-  p.page_mul = (uint32_t)((((uint64_t)1 << (31 + s)) + a.page_size - 1) / a.page_size);
-  p.page_shift = 31 + s;
+  divider(a.page_size, p.page_mul, p.page_shift);
+  divider(a.scale_block > 0 ? a.scale_block : 1, p.blk_mul, p.blk_shift);
   const size_t need = attn_workspace_bytes(a);
   p.shares = a.batch;
   p.plan = nullptr;
@@ -187,7 +196,11 @@ hipError_t launch_attn_decode(const gdn_attn_decode_args& a, hipStream_t stream)
   const int64_t units = (int64_t)p.shares * p.hkv;
   const dim3 grid((unsigned)((units + per - 1) / per * 8 * nwg));
   hipError_t e;
-  if (a.cache_dtype == GDN_E4M3)
+  if (a.cache_dtype == GDN_I8)  // block scales always
+    e = a.io_dtype == GDN_BF16 ? launch_attn_bf16_i8_blocks(p, a.d, grid, stream) : launch_attn_f32_i8_blocks(p, a.d, grid, stream);
+  else if (a.scale_block > 0)
+    e = a.io_dtype == GDN_BF16 ? launch_attn_bf16_e4m3_blocks(p, a.d, grid, stream) : launch_attn_f32_e4m3_blocks(p, a.d, grid, stream);
+  else if (a.cache_dtype == GDN_E4M3)
     e = a.io_dtype == GDN_BF16 ? launch_attn_bf16_e4m3(p, a.d, grid, stream) : launch_attn_f32_e4m3(p, a.d, grid, stream);
   else
     e = a.io_dtype == GDN_BF16 ? launch_attn_bf16(p, a.d, grid, stream) : launch_attn_f32(p, a.d, grid, stream);

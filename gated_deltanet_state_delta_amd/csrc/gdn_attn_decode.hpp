@@ -36,11 +36,15 @@
 // the weights to 2^-16; the second MFMA is free next to the loads.
 #pragma once
 
-#include "gdn_device.hpp"
-#include "gdn_paged.hpp"
+#include <type_traits>
+
+#include "gdn_kv.hpp"
 
 namespace gdn {
 
+// BS: block scales.  A tile's are read one tile ahead, a key by each lane, and
+// go through LDS to the lanes that hold the key's scores: the key's factor
+// enters the score, the value's the weight before the product.
 struct AttnParams {
   const void* q;
   int64_t q_sb, q_st, q_sh;  // bytes
@@ -56,6 +60,10 @@ struct AttnParams {
   const int32_t* lens;
   const float* k_scale;
   const float* v_scale;
+  const float* k_blocks;  // block scales, [n_pages][hkv][nblk]
+  const float* v_blocks;
+  uint32_t blk_mul, blk_shift;  // j / scale_block, as j / page_size below
+  int nblk;
   float* part_o;   // [2 * shares][hkv][R][D]; the workspace's arrays are null when each row is one share
   float* part_ml;  // [2 * shares][hkv][R][2]
   int2* plan;      // [batch]: a row's first share and how many it lies in
@@ -184,13 +192,15 @@ __device__ __forceinline__ Raw<N> raw_load(const char* p) {
 
 typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
 typedef float f2 __attribute__((ext_vector_type(2)));
-struct e4m3 { uint8_t b; };
 
-// Elements 2i and 2i+1 of a piece as two packed bf16 (exact for e4m3).
+// Elements 2i and 2i+1 of a piece as two packed bf16 (exact for 8-bit types).
 template <typename KE, int N>
 __device__ __forceinline__ uint32_t bf_pair(const Raw<N>& r, int i) {
   if constexpr (sizeof(KE) == 2) return r.w[i];
-  else return __builtin_bit_cast(uint32_t, (i & 1) ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r.w[i >> 1], 1.0f, true)
+  else if constexpr (std::is_same<KE, i8>::value) {
+    const uint32_t w = r.w[i >> 1] >> (16 * (i & 1));
+    return __builtin_amdgcn_perm(__float_as_uint((float)(int8_t)(w >> 8)), __float_as_uint((float)(int8_t)w), 0x07060302u);
+  } else return __builtin_bit_cast(uint32_t, (i & 1) ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r.w[i >> 1], 1.0f, true)
                                                    : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r.w[i >> 1], 1.0f, false));
 }
 // Elements 2i and 2i+1 of an fp32 piece.
@@ -270,7 +280,7 @@ struct AttnCfg {
 // page: its base is a scalar and rows past the end read zeros through the
 // buffer's bound.  Otherwise each key's offset is looked up by one lane and
 // passed through LDS.
-template <typename IO, typename KE, int D, bool UNI, int KIND>
+template <typename IO, typename KE, int D, bool UNI, int KIND, bool BS>
 __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND>::OCC)) attn_decode_kernel(AttnParams p) {
   typedef AttnCfg<IO, KE, D, KIND> C;
   constexpr int KT = C::KT, NT = C::NT, NC = C::NC, KW = C::KW, VW = C::VW, U = C::U, NA = C::NA, ES = C::ES;
@@ -281,6 +291,7 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND>::OCC)) attn_dec
   constexpr bool BF = C::BF, MT = KIND > 0, ONCE = KIND < 2 || (KIND == 2 && RT == 2);
   constexpr uint64_t kNone = ~0ull;
   __shared__ uint64_t offs[UNI ? 1 : 4][2][2][UNI ? 1 : KT];  // [wave][parity][K, V][key]
+  __shared__ __align__(16) float blocks[BS ? 4 : 1][2][BS ? KT : 4];  // [wave][K, V][key]: a tile's scales
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -296,7 +307,7 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND>::OCC)) attn_dec
   if (share_id >= p.shares || rt >= p.ntile) return;
   AttnShare share = attn_share<KT>(p, share_id, lane);
 
-  const float s_scale = p.scale_log2 * (p.k_scale ? p.k_scale[h] : 1.0f);
+  const float s_scale = BS ? p.scale_log2 : p.scale_log2 * (p.k_scale ? p.k_scale[h] : 1.0f);
 
   while (share.n > 0) {
     const int b = share.b, len = attn_len(p, b), row_steps = attn_steps<KT>(len), at = share.at;
@@ -453,17 +464,41 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND>::OCC)) attn_dec
         }
     };
 
+    // The block scales of a tile, lane l's those of key l: 0 where no key is held.
+    struct Scales { float k, v; };
+    auto load_scales = [&](int ent, int key0) {
+      const int key = key0 + lane;
+      Scales o = {0.f, 0.f};
+      if (lane < KT && key < len && ent >= 0 && ent < p.n_pages) {
+        const int blk = (int)(((uint64_t)(uint32_t)key * p.blk_mul) >> p.blk_shift) - page_of(key) * p.nblk;
+        const int64_t at = ((int64_t)ent * p.hkv + h) * p.nblk + blk;
+        o.k = p.k_blocks[at];
+        o.v = p.v_blocks[at];
+      }
+      return o;
+    };
+    auto lane_ent = [&](const Ents& en) {  // UNI: the entry of key `lane`
+      int e = en.e[0];
+#pragma unroll
+      for (int n = 1; n < NT; ++n) e = lane >> 4 == n ? en.e[n] : e;
+      return e;
+    };
+
     Ents ent_cur = {}, ent_next = {};
+    Scales sc = {};
     int ent1_next = 0;
     int par = 0;
     if (c0 < c1) {
       if constexpr (UNI) {
         ent_cur = load_ents(c0);
         issue_k_uni(ent_cur, c0);
+        if constexpr (BS) sc = load_scales(lane_ent(ent_cur), c0);
         ent_next = load_ents(c0 + KT);
       } else {
-        publish(load_ent1(c0), c0, 0);
+        const int ent1 = load_ent1(c0);
+        publish(ent1, c0, 0);
         issue_k_any(0);
+        if constexpr (BS) sc = load_scales(ent1, c0);
         ent1_next = load_ent1(c0 + KT);
       }
     }
@@ -505,13 +540,30 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND>::OCC)) attn_dec
           }
         }
       }
+      f4 ks[BS ? NT : 1], vs[BS ? NT : 1];  // of the lane's keys
+      if constexpr (BS) {
+        __builtin_amdgcn_wave_barrier();
+        if (lane < KT) {
+          blocks[wave][0][lane] = sc.k * s_scale;
+          blocks[wave][1][lane] = sc.v;
+        }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          ks[n] = *reinterpret_cast<const f4*>(&blocks[wave][0][16 * n + 4 * g]);
+          vs[n] = *reinterpret_cast<const f4*>(&blocks[wave][1][16 * n + 4 * g]);
+        }
+      }
       // The next tile's keys into the registers that the scores just read.
       uint32_t sub_ok = ~0u;
       if constexpr (UNI) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
           if (ent_cur.e[n] < 0 || ent_cur.e[n] >= p.n_pages) sub_ok &= ~(1u << n);
-        if (key0 + KT < c1) issue_k_uni(ent_next, key0 + KT);
+        if (key0 + KT < c1) {
+          issue_k_uni(ent_next, key0 + KT);
+          if constexpr (BS) sc = load_scales(lane_ent(ent_next), key0 + KT);
+        }
         ent_cur = ent_next;
         ent_next = load_ents(key0 + 2 * KT);
       } else {
@@ -519,6 +571,7 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND>::OCC)) attn_dec
         if (key0 + KT < c1) {
           publish(ent1_next, key0 + KT, par);
           issue_k_any(par);
+          if constexpr (BS) sc = load_scales(ent1_next, key0 + KT);
           ent1_next = load_ent1(key0 + 2 * KT);
         }
       }
@@ -533,7 +586,7 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND>::OCC)) attn_dec
           for (int j = 0; j < 4; ++j) {
             const int key = key0 + 16 * n + 4 * g + j;
             const bool sees = key < lim[q] && (UNI ? ((sub_ok >> n) & 1) != 0 : ((held >> (4 * n + j)) & 1) != 0);
-            s[q][n][j] = sees ? s[q][n][j] * s_scale : -__builtin_inff();
+            s[q][n][j] = sees ? s[q][n][j] * (BS ? ks[BS ? n : 0][j] : s_scale) : -__builtin_inff();
             mx = fmaxf(mx, s[q][n][j]);
           }
         mx = max_over_g(mx);
@@ -553,6 +606,9 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND>::OCC)) attn_dec
           for (int j = 0; j < 4; ++j) {
             s[q][n][j] = exp2_hw(s[q][n][j] - mu);
             l[q] += s[q][n][j];
+            // a key that another of the new tokens sees may have a scale that is not finite
+            if constexpr (BS)
+              s[q][n][j] = !MT || key0 + 16 * n + 4 * g + j < lim[q] ? s[q][n][j] * vs[BS ? n : 0][j] : 0.f;
           }
       }
       if constexpr (!UNI) {  // a row that is not there must not reach the product
@@ -571,7 +627,7 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND>::OCC)) attn_dec
       // such a value is present, each token takes the product on its own, with
       // the values that it does not see replaced by zeros.
       bool apart = false;
-      if (MT && key0 + KT > len - p.T + 1) {
+      if (MT && !std::is_same<KE, i8>::value && key0 + KT > len - p.T + 1) {
         bool odd = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -746,12 +802,12 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND>::OCC)) attn_dec
   }
 }
 
-template <typename IO, typename KE>
+template <typename IO, typename KE, bool BS = false>
 hipError_t launch_attn_t(const AttnParams& p, int d, dim3 grid, hipStream_t stream) {
   const bool uni = p.page_size % 16 == 0;
   const int kind = attn_kind(p.T, p.R);
 #define GDN_ATTN_LAUNCH(DD, UNI, KIND) \
-  hipLaunchKernelGGL((attn_decode_kernel<IO, KE, DD, UNI, KIND>), grid, dim3(256), 0, stream, p)
+  hipLaunchKernelGGL((attn_decode_kernel<IO, KE, DD, UNI, KIND, BS>), grid, dim3(256), 0, stream, p)
 #define GDN_ATTN_KINDS(DD, UNI)                     \
   if (kind == 0) GDN_ATTN_LAUNCH(DD, UNI, 0);       \
   else if (kind == 1) GDN_ATTN_LAUNCH(DD, UNI, 1);  \
@@ -782,5 +838,10 @@ hipError_t launch_attn_bf16(const AttnParams& p, int d, dim3 grid, hipStream_t s
 hipError_t launch_attn_f32(const AttnParams& p, int d, dim3 grid, hipStream_t stream);
 hipError_t launch_attn_bf16_e4m3(const AttnParams& p, int d, dim3 grid, hipStream_t stream);
 hipError_t launch_attn_f32_e4m3(const AttnParams& p, int d, dim3 grid, hipStream_t stream);
+// with block scales
+hipError_t launch_attn_bf16_e4m3_blocks(const AttnParams& p, int d, dim3 grid, hipStream_t stream);
+hipError_t launch_attn_f32_e4m3_blocks(const AttnParams& p, int d, dim3 grid, hipStream_t stream);
+hipError_t launch_attn_bf16_i8_blocks(const AttnParams& p, int d, dim3 grid, hipStream_t stream);
+hipError_t launch_attn_f32_i8_blocks(const AttnParams& p, int d, dim3 grid, hipStream_t stream);
 
 }  // namespace gdn

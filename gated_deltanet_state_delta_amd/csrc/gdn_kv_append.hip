@@ -7,8 +7,7 @@
 // workgroup takes a run of tokens: one thread a token finds its row, position
 // and page and leaves the two row offsets in LDS, then every thread copies
 // pieces of 8 elements (16-byte loads and stores for bf16).
-#include "gdn_device.hpp"
-#include "gdn_paged.hpp"
+#include "gdn_kv.hpp"
 
 namespace gdn {
 
@@ -29,63 +28,6 @@ struct AppendParams {
   int batch, T, hkv, d, n_pages, page_size, cap, run;
 };
 
-// 8 elements of a new token, read once.
-template <typename IO> struct Piece;
-template <> struct Piece<__bf16> {
-  u32x4 r;
-  __device__ __forceinline__ void load(const __bf16* p) { r = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p)); }
-  __device__ __forceinline__ float at(int i) const {
-    return __uint_as_float((i & 1) ? r[i >> 1] & 0xffff0000u : r[i >> 1] << 16);
-  }
-  __device__ __forceinline__ void store(__bf16* p) const { *reinterpret_cast<u32x4*>(p) = r; }
-};
-template <> struct Piece<float> {
-  f4 r[2];
-  __device__ __forceinline__ void load(const float* p) {
-    r[0] = ld_nt(p);
-    r[1] = ld_nt(p + 4);
-  }
-  __device__ __forceinline__ float at(int i) const { return r[i >> 2][i & 3]; }
-  __device__ __forceinline__ void store(float* p) const {
-    reinterpret_cast<f4*>(p)[0] = r[0];
-    reinterpret_cast<f4*>(p)[1] = r[1];
-  }
-};
-
-// Beyond +-448 clamped; NaN stays NaN.
-__device__ __forceinline__ float e4m3_clamp(float q) {
-  const float c = __builtin_amdgcn_fmed3f(q, -448.0f, 448.0f);
-  return q != q ? q : c;
-}
-
-// 8 quotients x / scale in e4m3, round to nearest even.  They come from a
-// product with 1 / scale, at most 3 units in the last place off; e4m3's values
-// and the midpoints between them have 19 zero bits at the end of an fp32
-// mantissa, so only a product within 16 units of such a number can round
-// otherwise than the quotient, and then the lane divides (IEEE division, about
-// 12 instructions each: 57 us instead of 40 for 32768 tokens of 8 heads of 128
-// with it alone).  inv is 0 where 1 / scale is not a normal number: always divide.
-template <typename IO>
-__device__ __forceinline__ uint2 e4m3_quotients(const Piece<IO>& x, float scale, float inv) {
-  float q[8];
-  uint32_t near = 0x7ffffu;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    q[i] = x.at(i) * inv;
-    near = min(near, (__float_as_uint(q[i]) + 16u) & 0x7ffffu);
-  }
-  if (near < 32u || inv == 0.f) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = x.at(i) / scale;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = e4m3_clamp(q[i]);
-  uint32_t lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false), hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], 0, false);
-  lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo, true);
-  hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[6], q[7], hi, true);
-  return make_uint2(lo, hi);
-}
-
 constexpr int kAppendRun = 64;  // most tokens of one workgroup
 
 template <typename IO, typename KE>
@@ -97,26 +39,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendParams p) {
     const int64_t i = t0 + threadIdx.x;
     int b;
     int64_t back;  // tokens from this one to its row's end
-    bool ok = true;
-    if (!p.cu) {
-      b = (int)(i / p.T);
-      back = p.T - i % p.T;
-    } else {
-      // the last row that starts at or before token i (offsets clamped to
-      // [0, total]); a token past that row's end belongs to none.  Offsets that
-      // decrease mislead the search, and the check of the range then leaves the
-      // token out.
-      int lo = 0, hi = p.batch;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (min(max((int64_t)p.cu[mid], (int64_t)0), p.total) <= i) lo = mid;
-        else hi = mid;
-      }
-      b = lo;
-      const int64_t s0 = min(max((int64_t)p.cu[b], (int64_t)0), p.total), s1 = min(max((int64_t)p.cu[b + 1], (int64_t)0), p.total);
-      ok = s0 <= i && i < s1;
-      back = s1 - i;
-    }
+    bool ok = token_row(p, i, b, back);
     const int64_t pos = (int64_t)p.lens[b] - back;
     ok = ok && pos >= 0 && pos < p.cap;
     uint64_t ko = 0, vo = 0;
@@ -174,9 +97,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendParams p) {
     for (int k = 0; k < 4; ++k) {
       if (!dst[k]) continue;
       if constexpr (sizeof(KE) == 1) {
-        const float one = __builtin_amdgcn_rcpf(scale[k]);
-        const float inv = fabsf(one) >= 1.2e-38f && fabsf(one) <= 3.0e38f ? one : 0.f;
-        *reinterpret_cast<uint2*>(dst[k]) = e4m3_quotients(x[k], scale[k], inv);
+        *reinterpret_cast<uint2*>(dst[k]) = e4m3_quotients(x[k], scale[k], normal_rcp(scale[k]));
       } else {
         x[k].store(dst[k]);
       }

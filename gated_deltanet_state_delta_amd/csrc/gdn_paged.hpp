@@ -13,6 +13,10 @@ namespace gdn {
 size_t attn_workspace_bytes(const gdn_attn_decode_args& args);
 hipError_t launch_attn_decode(const gdn_attn_decode_args& args, hipStream_t stream);
 hipError_t launch_kv_append(const gdn_kv_append_args& args, hipStream_t stream);
+// The same with block scales.
+hipError_t launch_kv_quantise(const gdn_kv_append_args& args, hipStream_t stream);
+hipError_t launch_kv_read(const gdn_kv_read_args& args, hipStream_t stream);
+hipError_t launch_rope(const gdn_rope_args& args, hipStream_t stream);
 
 hipError_t launch_pages_copy(void* pool, int64_t page_bytes, int64_t stride, int n_pages, const int32_t* src,
                              const int32_t* dst, int64_t n, hipStream_t stream);

@@ -7,6 +7,7 @@ As in the rest of the binding, only arguments are marshalled here
 
   attn_decode(q, k_cache, v_cache, page_table, lens, ...) -> out | (out, lse)
   kv_append(k, v, k_cache, v_cache, page_table, lens, ...) -> (k_cache, v_cache)
+  kv_read(k_cache, v_cache, page_table, lens, tokens, ...) -> (k, v)
   pages_copy(pool, src, dst) -> pool
   pages_extend(page_table, lens, refs, add, page_size) -> (page_table, lens, refs, ok)
   pages_fork(page_table, lens, refs, parent, page_size) -> (page_table, lens, refs, src, dst)
@@ -23,7 +24,7 @@ from . import _lib
 
 _I32_MIN, _I32_MAX = -(1 << 31), (1 << 31) - 1
 _IO = {torch.float32: _lib.GDN_F32, torch.bfloat16: _lib.GDN_BF16}
-_CACHE = {**_IO, torch.float8_e4m3fn: _lib.GDN_E4M3}
+_CACHE = {**_IO, torch.float8_e4m3fn: _lib.GDN_E4M3, torch.int8: _lib.GDN_I8}
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
@@ -101,7 +102,8 @@ def _cache_strides(c, shape, name):
 
 def _caches(io, k_cache, v_cache, shape, k_scale, v_scale, hkv, d):
     """Checks of a key and a value cache and their scales: (the cache type's
-    code, k_scale, v_scale, the K and V strides)."""
+    code, the factors a head (k_scale, v_scale), the block scales (tokens of a
+    block, k_scale, v_scale), the K and V strides)."""
     if len(shape) != 4 or shape[2] != hkv or shape[3] != d:
         raise ValueError("k_cache must be [n_pages, page_size, %d, %d], got %s" % (hkv, d, tuple(shape)))
     dtype = k_cache.dtype
@@ -109,23 +111,41 @@ def _caches(io, k_cache, v_cache, shape, k_scale, v_scale, hkv, d):
         raise ValueError("k_cache and v_cache must share shape and dtype")
     if shape[1] < 1:
         raise ValueError("page_size must be at least 1")
-    if dtype is torch.float8_e4m3fn:
+    blocks = (0, None, None)
+    if dtype is torch.float8_e4m3fn or dtype is torch.int8:
         if k_scale is None or v_scale is None:
-            raise ValueError("float8_e4m3fn caches need k_scale and v_scale")
-        k_scale, v_scale = _scale(k_scale, "k_scale", hkv), _scale(v_scale, "v_scale", hkv)
+            raise ValueError("%s caches need k_scale and v_scale" % dtype)
+        if k_scale.dim() == 3 or v_scale.dim() == 3 or dtype is torch.int8:
+            blocks = (_block_scales(k_scale, v_scale, shape), k_scale, v_scale)
+            k_scale = v_scale = None
+        else:
+            k_scale, v_scale = _scale(k_scale, "k_scale", hkv), _scale(v_scale, "v_scale", hkv)
     elif dtype is not io:
-        raise ValueError("the caches must have the inputs' dtype or float8_e4m3fn, got %s" % dtype)
+        raise ValueError("the caches must have the inputs' dtype, float8_e4m3fn or int8, got %s" % dtype)
     elif k_scale is not None or v_scale is not None:
-        raise ValueError("k_scale and v_scale are for float8_e4m3fn caches")
+        raise ValueError("k_scale and v_scale are for 8-bit caches")
     ks = _cache_strides(k_cache, shape, "k_cache")
     vs = _cache_strides(v_cache, shape, "v_cache")
-    return _CACHE[dtype], k_scale, v_scale, ks, vs
+    return _CACHE[dtype], (k_scale, v_scale), blocks, ks, vs
 
 
 def _scale(t, name, hkv):
     if t.shape != (hkv,) or t.dtype != torch.float32:
         raise ValueError("%s must be [%d] float32" % (name, hkv))
     return t if t.is_contiguous() else t.contiguous()
+
+
+def _block_scales(k_scale, v_scale, shape):
+    """Tokens of a block of the block scales of a cache of this shape."""
+    n_pages, page, hkv, _ = shape
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if (t.dim() != 3 or t.shape[0] != n_pages or t.shape[1] != hkv or t.shape[2] < 1 or page % t.shape[2]
+                or t.dtype != torch.float32 or not t.is_contiguous()):
+            raise ValueError("%s must be contiguous float32 [%d, %d, blocks], blocks dividing page_size %d, got %s %s"
+                             % (name, n_pages, hkv, page, t.dtype, tuple(t.shape)))
+    if k_scale.shape != v_scale.shape:
+        raise ValueError("k_scale and v_scale must share their shape")
+    return page // k_scale.shape[2]
 
 
 def _rows16(t):
@@ -162,7 +182,7 @@ def attn_decode_args(q, k_cache, v_cache, page_table, lens, *, scale=None, k_sca
     if len(cs) != 4:
         raise ValueError("k_cache must be [n_pages, page_size, hkv, d]")
     n_pages, page, hkv, _ = cs
-    cache_dtype, k_scale, v_scale, ks, vs = _caches(dtype, k_cache, v_cache, cs, k_scale, v_scale, hkv, d)
+    cache_dtype, factors, blocks, ks, vs = _caches(dtype, k_cache, v_cache, cs, k_scale, v_scale, hkv, d)
     q = _rows16(q)
     table, table_stride, max_pages = _table(page_table, B)
     lens = _i32(lens, "lens", (B,))
@@ -177,9 +197,9 @@ def attn_decode_args(q, k_cache, v_cache, page_table, lens, *, scale=None, k_sca
     a = _lib.AttnDecodeArgs(
         B, T, hq, hkv, d, _IO[dtype], cache_dtype, d ** -0.5 if scale is None else float(scale),
         q.data_ptr(), qs[0], qs[1], qs[2], k_cache.data_ptr(), *ks, v_cache.data_ptr(), *vs,
-        n_pages, page, max_pages, table.data_ptr(), table_stride, lens.data_ptr(), _ptr(k_scale), _ptr(v_scale),
-        out.data_ptr(), _ptr(lse))
-    return a, (q, table, lens, k_scale, v_scale), out
+        n_pages, page, max_pages, table.data_ptr(), table_stride, lens.data_ptr(), _ptr(factors[0]), _ptr(factors[1]),
+        out.data_ptr(), _ptr(lse), None, 0, blocks[0], _ptr(blocks[1]), _ptr(blocks[2]))
+    return a, (q, table, lens, factors, blocks), out
 
 
 def attn_decode(q, k_cache, v_cache, page_table, lens, *, scale=None, k_scale=None, v_scale=None, out=None,
@@ -187,10 +207,12 @@ def attn_decode(q, k_cache, v_cache, page_table, lens, *, scale=None, k_scale=No
     """Softmax attention of each row's newest T tokens over a paged cache.
 
     q [B, T, hq, d] float32 or bfloat16, 1 <= T <= 64, d in {32, 64, 128, 256};
-    k_cache, v_cache [n_pages, page_size, hkv, d] in q's dtype or float8_e4m3fn
-    (then with k_scale, v_scale [hkv] float32, the factors of the stored
-    values), any page_size, and with heads before tokens in memory where the
-    tensor is such a view; page_table [B, max_pages], lens [B] int32 or int64.
+    k_cache, v_cache [n_pages, page_size, hkv, d] in q's dtype, float8_e4m3fn
+    or int8, any page_size, and with heads before tokens in memory where the
+    tensor is such a view.  8-bit caches come with k_scale, v_scale float32, the
+    factors of the stored values: [n_pages, hkv, blocks], one for each block of
+    page_size / blocks tokens (at most 65536) and head, as kv_append sets them,
+    or for float8_e4m3fn [hkv], one for each head.  page_table [B, max_pages], lens [B] int32 or int64.
     The cache holds the new tokens already (kv_append): token t of row b is
     position lens[b] - T + t and sees the positions up to its own.  Query head
     h reads key-value head h*hkv//hq.  scale None means 1/sqrt(d).
@@ -268,7 +290,7 @@ def kv_append_args(k, v, k_cache, v_cache, page_table, lens, *, cu_seqlens=None,
         total, hkv, d = shape
         cu_seqlens = _i32(cu_seqlens, "cu_seqlens", (B + 1,))
     cs = k_cache.shape
-    cache_dtype, k_scale, v_scale, kcs, vcs = _caches(dtype, k_cache, v_cache, cs, k_scale, v_scale, hkv, d)
+    cache_dtype, factors, blocks, kcs, vcs = _caches(dtype, k_cache, v_cache, cs, k_scale, v_scale, hkv, d)
     k, v = _rows16(k), _rows16(v)
     table, table_stride, max_pages = _table(page_table, B)
     lens = _i32(lens, "lens", (B,))
@@ -276,8 +298,9 @@ def kv_append_args(k, v, k_cache, v_cache, page_table, lens, *, cu_seqlens=None,
         total, B, hkv, d, _IO[dtype], cache_dtype, k.data_ptr(), *_token_strides(k, hkv, d),
         v.data_ptr(), *_token_strides(v, hkv, d),
         _ptr(cu_seqlens), k_cache.data_ptr(), *kcs, v_cache.data_ptr(), *vcs, cs[0], cs[1], max_pages,
-        table.data_ptr(), table_stride, lens.data_ptr(), _ptr(k_scale), _ptr(v_scale))
-    return a, (k, v, cu_seqlens, table, lens, k_scale, v_scale)
+        table.data_ptr(), table_stride, lens.data_ptr(), _ptr(factors[0]), _ptr(factors[1]), blocks[0], _ptr(blocks[1]),
+        _ptr(blocks[2]))
+    return a, (k, v, cu_seqlens, table, lens, factors, blocks)
 
 
 def kv_append(k, v, k_cache, v_cache, page_table, lens, *, cu_seqlens=None, k_scale=None, v_scale=None,
@@ -290,8 +313,16 @@ def kv_append(k, v, k_cache, v_cache, page_table, lens, *, cu_seqlens=None, k_sc
     row b's n tokens go to positions lens[b] - n .. lens[b] - 1 of its pages;
     tokens whose position lies outside the table or whose table entry is
     outside the cache are not written.  Caches, page_table and scales as for
-    attn_decode; a float8_e4m3fn cache stores x / scale rounded to nearest
-    even and clamped to +-448.  Returns (k_cache, v_cache).
+    attn_decode; an 8-bit cache stores x / scale rounded to nearest even and
+    clamped to +-448 (float8_e4m3fn) or +-127 (int8).
+
+    Block scales ([n_pages, hkv, blocks]) are updated in place: with a the
+    largest finite |x| of a block's new tokens and head, its scale becomes the
+    smallest power of two with a <= 448 scale (float8_e4m3fn) or a / 127 (int8),
+    not below 2^-126 and, where the row has older tokens in the block, not below
+    what it was; older tokens' codes are rounded again where it grew.  The first
+    slot of a block starts it anew, so pages need no clearing.  NaN in a token
+    makes the scale of an int8 block NaN.  Returns (k_cache, v_cache).
     """
     dev = k.device
     ctx = _on(stream, dev, (v, k_cache, v_cache, page_table, lens, cu_seqlens, k_scale, v_scale))
@@ -304,6 +335,73 @@ def kv_append(k, v, k_cache, v_cache, page_table, lens, *, cu_seqlens=None, k_sc
     _checked(_library().gdn_kv_append(byref(a), _raw_stream(dev.index)))
     del keep
     return k_cache, v_cache
+
+
+def kv_read_args(k_cache, v_cache, page_table, lens, tokens, *, cu_seqlens=None, dtype=None, k_scale=None,
+                 v_scale=None, out=None):
+    """Validate shapes and build the gdn_kv_read_args struct (device-agnostic):
+    returns (args, tensors to keep alive, (k, v))."""
+    cs = k_cache.shape
+    if len(cs) != 4:
+        raise ValueError("k_cache must be [n_pages, page_size, hkv, d]")
+    n_pages, page, hkv, d = cs
+    if lens.dim() != 1:
+        raise ValueError("lens must be [B]")
+    B = lens.shape[0]
+    if int(tokens) != tokens or tokens < 0:
+        raise ValueError("tokens must be a whole number of at least 0, got %s" % (tokens,))
+    tokens = int(tokens)
+    if dtype is None:
+        dtype = out[0].dtype if out is not None else k_cache.dtype if k_cache.dtype in _IO else torch.bfloat16
+    if dtype not in _IO:
+        raise ValueError("unsupported dtype %s (float32 or bfloat16)" % dtype)
+    cache_dtype, factors, blocks, kcs, vcs = _caches(dtype, k_cache, v_cache, cs, k_scale, v_scale, hkv, d)
+    if cu_seqlens is None:
+        total, shape = B * tokens, (B, tokens, hkv, d)
+    else:
+        total, shape = tokens, (tokens, hkv, d)
+        cu_seqlens = _i32(cu_seqlens, "cu_seqlens", (B + 1,))
+    new = out is None
+    if new:
+        out = tuple(torch.empty(shape, dtype=dtype, device=k_cache.device) for _ in range(2))
+    else:
+        for t in out:
+            if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or t.data_ptr() % 16:
+                raise ValueError("out must be two contiguous, 16-byte aligned %s %s" % (dtype, tuple(shape)))
+    table, table_stride, max_pages = _table(page_table, B)
+    lens = _i32(lens, "lens", (B,))
+    a = _lib.KvReadArgs(
+        total, B, hkv, d, _IO[dtype], cache_dtype, out[0].data_ptr(), hkv * d, d, out[1].data_ptr(), hkv * d, d,
+        _ptr(cu_seqlens), k_cache.data_ptr(), *kcs, v_cache.data_ptr(), *vcs, n_pages, page, max_pages,
+        table.data_ptr(), table_stride, lens.data_ptr(), _ptr(factors[0]), _ptr(factors[1]), blocks[0], _ptr(blocks[1]),
+        _ptr(blocks[2]), int(new))
+    return a, (cu_seqlens, table, lens, factors, blocks), tuple(out)
+
+
+def kv_read(k_cache, v_cache, page_table, lens, tokens, *, cu_seqlens=None, dtype=None, k_scale=None, v_scale=None,
+            out=None, stream=None):
+    """Read tokens back out of their pages: the inverse of kv_append.
+
+    tokens: how many newest tokens of every row, or with non-decreasing
+    cu_seqlens [B + 1] the packed total.  Row b's n tokens are those of positions
+    lens[b] - n .. lens[b] - 1; positions that hold nothing (below 0, past the
+    table, a table entry outside the cache) give zeros.  Caches, page_table and
+    scales as for attn_decode; 8-bit values are multiplied by their scale.  dtype
+    (None: the caches', bfloat16 for 8-bit ones): of the result, one rounding.
+    out: (k, v) to write to; tokens of no row are left as they were there, and
+    zeros in new ones.  Returns (k, v): [B, tokens, hkv, d], or [tokens, hkv, d].
+    """
+    dev = k_cache.device
+    ctx = _on(stream, dev, (v_cache, page_table, lens, cu_seqlens, k_scale, v_scale) + tuple(out or ()))
+    if ctx is not None:
+        with ctx:
+            return kv_read(k_cache, v_cache, page_table, lens, tokens, cu_seqlens=cu_seqlens, dtype=dtype,
+                           k_scale=k_scale, v_scale=v_scale, out=out)
+    a, keep, out = kv_read_args(k_cache, v_cache, page_table, lens, tokens, cu_seqlens=cu_seqlens, dtype=dtype,
+                                k_scale=k_scale, v_scale=v_scale, out=out)
+    _checked(_library().gdn_kv_read(byref(a), _raw_stream(dev.index)))
+    del keep
+    return out
 
 
 def _page_block(pool):

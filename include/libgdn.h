@@ -49,8 +49,9 @@ typedef enum {
   GDN_ERR_HIP = 6          /* a HIP launch failed; gdn_last_error() has the text   */
 } gdn_status;
 
-/* GDN_E4M3 (OCP 8-bit float, largest value 448) is a type of key-value caches only. */
-typedef enum { GDN_F32 = 0, GDN_BF16 = 1, GDN_E4M3 = 2 } gdn_dtype;
+/* GDN_E4M3 (OCP 8-bit float, largest value 448) and GDN_I8 (whole numbers of
+ * -127 to 127) are types of key-value caches only. */
+typedef enum { GDN_F32 = 0, GDN_BF16 = 1, GDN_E4M3 = 2, GDN_I8 = 3 } gdn_dtype;
 
 /* update_rule of "com.microsoft.GatedDeltaNet" (Attributes): which terms of
  *   S_t = exp(g_t) S_{t-1} + k_t (beta_t (v_t - exp(g_t) S_{t-1}^T k_t))^T
@@ -426,10 +427,19 @@ gdn_status gdn_conv1d(const gdn_conv1d_args* args, void* stream);
  *   page_table  [batch, max_pages] int32, rows page_table_stride apart
  *   lens        [batch] int32
  *   k_scale, v_scale  [hkv] fp32: the factor of each head's stored values,
- *               given for GDN_E4M3 caches and NULL for the others
+ *               given for GDN_E4M3 caches without block scales and NULL for
+ *               the others
+ * An 8-bit cache (GDN_E4M3, and GDN_I8 always) may instead have a scale for
+ * each block of scale_block tokens of a page and head; scale_block divides
+ * page_size and is at most 65536, and 0 means that there are no block scales:
+ *   k_block_scale, v_block_scale  [n_pages, hkv, page_size / scale_block] fp32,
+ *               dense: slot i of a page lies in block i / scale_block.  A page's
+ *               scales are one dense block, for gdn_pages_copy beside its codes.
+ * gdn_kv_append sets them from what it writes; a stored value is its code
+ * times its block's scale.
  * Common requirements: page_size and max_pages * page_size at most 2^30; d in
  * {32, 64, 128, 256}; hq a multiple of hkv (query head h reads key-value head
- * h*hkv/hq); a cache has io_dtype's type or GDN_E4M3; caches, q, k, v and out
+ * h*hkv/hq); a cache has io_dtype's type or an 8-bit one; caches, q, k, v and out
  * 16-byte aligned, their strides non-negative multiples of 16 bytes; a cache's
  * token strides in [d, 2^23) and its head strides in [d, 2^40) elements, its rows
  * apart and its page stride not smaller than a page.
@@ -443,6 +453,8 @@ gdn_status gdn_conv1d(const gdn_conv1d_args* args, void* stream);
  *     s_j = scale * k_scale[g] * <q[b,t,h], K[b,j,g]>,   g = h*hkv/hq
  *     out[b,t,h] = v_scale[g] * sum_j e^{s_j} V[b,j,g] / sum_j e^{s_j}
  *     lse[b,t,h] = log sum_j e^{s_j}
+ * With block scales k_scale[g] is that of key j's block, and v_scale[g] stands
+ * inside the sum; scales of blocks that hold no token of the row are not read.
  * A token that sees nothing (a row of no tokens, a position below 0, only
  * invalid pages), or whose scores are all -inf, gets zeros and lse -inf.  A NaN
  * in a token's query or in a key that it sees makes its result and lse NaN.
@@ -487,6 +499,9 @@ typedef struct {
   float* lse;
   void* workspace;
   size_t workspace_bytes;
+  int32_t scale_block;      /* appended; 0: no block scales */
+  const float* k_block_scale;
+  const float* v_block_scale;
 } gdn_attn_decode_args;
 
 size_t gdn_attn_decode_workspace_size(const gdn_attn_decode_args* args);
@@ -500,6 +515,23 @@ gdn_status gdn_attn_decode(const gdn_attn_decode_args* args, void* stream);
  * or past the table, or whose page entry is invalid, are not written.  An
  * e4m3 cache stores x / scale of the head, rounded to nearest even, clamped
  * to +-448 (NaN stays NaN); others store x as it is.
+ *
+ * With block scales the call sets the scale of every block that it writes to,
+ * for each head, from the largest finite |x| of the block's new tokens, a:
+ *     GDN_E4M3:  need = the smallest power of two with a <= 448 need
+ *     GDN_I8:    need = a * (1 / 127), both fp32
+ *     s = max(need, 2^-126, and, where the row has older tokens in the block,
+ *             its scale until now)
+ * and stores x / s rounded to nearest even, clamped to +-448 or +-127.  Where
+ * the scale of a block with older tokens changes, their codes c become
+ * c * s_old / s (fp32), rounded and clamped alike.  A power of two costs an 8-bit
+ * float no precision, and a step from one to a larger one keeps the older
+ * values, but for those that fall below the type's smallest normal number;
+ * whole numbers take the closest scale and round again.  A block's first new
+ * token at the block's first slot starts it anew: what its scale and codes held
+ * does not matter.  NaN is a code of GDN_E4M3; GDN_I8 has none, so NaN in a
+ * token makes its block's scale NaN.  A scale that is NaN stays so.
+ * total_tokens / scale_block + 2 * batch is below 2^29.
  *
  *   k, v  [total_tokens, hkv, d] io_dtype, strides {token, head}
  *   cu_seqlens  [batch + 1] int32, non-decreasing: row b's tokens are
@@ -531,9 +563,106 @@ typedef struct {
   const int32_t* lens;
   const float* k_scale;
   const float* v_scale;
+  int32_t scale_block;      /* appended; 0: no block scales */
+  float* k_block_scale;
+  float* v_block_scale;
 } gdn_kv_append_args;
 
 gdn_status gdn_kv_append(const gdn_kv_append_args* args, void* stream);
+
+/* ----------------------------------------------------------------------------
+ * gdn_kv_read -- tokens read back out of their pages, the way that
+ * gdn_kv_append put them in.
+ *
+ * Row b's n_b tokens are those of positions lens[b] - n_b .. lens[b] - 1, in
+ * order, of any type of cache: k and v get the stored values (the code times
+ * its scale for 8-bit caches), rounded once to io_dtype.  Tokens at positions
+ * that hold nothing (negative, past the table, an invalid page entry) get zeros.
+ *
+ *   k, v  [total_tokens, hkv, d] io_dtype, strides {token, head}; written
+ *   cu_seqlens  as for gdn_kv_append; tokens of no row are left as they were,
+ *         or get zeros with zero_rest != 0
+ * k and v must not overlap each other or the caches (not checked).  cache_dtype
+ * is io_dtype's type or an 8-bit one.  total_tokens is at most 2^28.  batch == 0
+ * or total_tokens == 0 is a no-op.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int64_t total_tokens;
+  int32_t batch, hkv, d;
+  int32_t io_dtype, cache_dtype;
+  void* k;
+  int64_t k_stride_token, k_stride_head;
+  void* v;
+  int64_t v_stride_token, v_stride_head;
+  const int32_t* cu_seqlens;
+  const void* k_cache;
+  int64_t kc_stride_page, kc_stride_token, kc_stride_head;
+  const void* v_cache;
+  int64_t vc_stride_page, vc_stride_token, vc_stride_head;
+  int32_t n_pages, page_size, max_pages;
+  const int32_t* page_table;
+  int64_t page_table_stride;
+  const int32_t* lens;
+  const float* k_scale;
+  const float* v_scale;
+  int32_t scale_block;
+  const float* k_block_scale;
+  const float* v_block_scale;
+  int32_t zero_rest;
+} gdn_kv_read_args;
+
+gdn_status gdn_kv_read(const gdn_kv_read_args* args, void* stream);
+
+/* ----------------------------------------------------------------------------
+ * gdn_rope -- rotary positions of queries and keys, before gdn_kv_append and
+ * gdn_attn_decode.
+ *
+ * Of each head vector the first rot dimensions are turned in pairs (x1, x2) by
+ * the angle pos * inv_freq[i], the others are copied:
+ *     y1 = factor * (x1 cos - x2 sin),   y2 = factor * (x1 sin + x2 cos)
+ * Pair i < rot / 2 is dimensions (i, i + rot / 2), with interleaved != 0 (2i,
+ * 2i + 1).  Angles are formed in fp64 (so that far positions keep theirs), sines
+ * and products in fp32; one rounding to io_dtype.
+ *
+ * A token's position is positions[token] where given, else it follows from lens
+ * as in gdn_kv_append: token i of row b's n_b is lens[b] - n_b + i.
+ *
+ *   q, q_out  [total_tokens, hq, d] io_dtype, strides {token, head}
+ *   k, k_out  [total_tokens, hkv, d] likewise; k NULL: queries only (hkv 0)
+ *   inv_freq  [rot / 2] fp64, in radians a position
+ *   positions [total_tokens] int32, or int64 with positions_i64 != 0, or NULL
+ *   lens [batch] int32, cu_seqlens [batch + 1] int32 or NULL: as for
+ *             gdn_kv_append (read where positions is NULL); tokens of no row
+ *             are left as they were in the outputs, or get zeros with
+ *             zero_rest != 0
+ * An output may be its input (equal pointer and strides); other overlaps are
+ * GDN_ERR_LAYOUT.  rot is even, 2 <= rot <= d <= 1024; hq + hkv at most 65536;
+ * total_tokens at most 2^24; pointers aligned to their element.  Rows of q_out
+ * and k_out must not overlap (not checked).  total_tokens == 0 is a no-op, and
+ * so is batch == 0 without positions.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int64_t total_tokens;
+  int32_t batch, hq, hkv, d, rot;
+  int32_t io_dtype, interleaved;
+  float factor;
+  const void* q;
+  int64_t q_stride_token, q_stride_head;
+  const void* k;
+  int64_t k_stride_token, k_stride_head;
+  void* q_out;
+  int64_t qo_stride_token, qo_stride_head;
+  void* k_out;
+  int64_t ko_stride_token, ko_stride_head;
+  const double* inv_freq;
+  const void* positions;
+  int32_t positions_i64;
+  const int32_t* lens;
+  const int32_t* cu_seqlens;
+  int32_t zero_rest;
+} gdn_rope_args;
+
+gdn_status gdn_rope(const gdn_rope_args* args, void* stream);
 
 /* ----------------------------------------------------------------------------
  * gdn_pages_copy -- contents of pages (or of state-pool and conv-state slots)
