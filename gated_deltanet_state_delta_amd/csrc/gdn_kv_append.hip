@@ -97,7 +97,9 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendParams p) {
     for (int k = 0; k < 4; ++k) {
       if (!dst[k]) continue;
       if constexpr (sizeof(KE) == 1) {
-        *reinterpret_cast<uint2*>(dst[k]) = e4m3_quotients(x[k], scale[k], normal_rcp(scale[k]));
+        float q[8];
+        e4m3_quotients(x[k], scale[k], normal_rcp(scale[k]), q);
+        *reinterpret_cast<uint2*>(dst[k]) = make_uint2(e4m3_pack(q), e4m3_pack(q + 4));
       } else {
         x[k].store(dst[k]);
       }
