@@ -30,48 +30,88 @@ struct RopeParams {
 constexpr int kRopeRun = 64;      // most tokens of one workgroup
 constexpr int kRopeAngles = 1024; // angles that it holds
 
-// V elements at p, as fp32; V = 1, or 16 bytes.
-template <int V> __device__ __forceinline__ void load_v(const float* p, float* x) {
+// V elements at p, which is aligned to one element (the hardware reads and
+// writes whole dwords at any address).
+template <typename IO, int V> struct RopeVec {
+  typedef IO type __attribute__((ext_vector_type(V), aligned(sizeof(IO))));
+};
+template <typename IO> struct RopeVec<IO, 1> { typedef IO type; };
+template <int V, typename IO> __device__ __forceinline__ void load_v(const IO* p, float* x) {
+  const auto t = __builtin_nontemporal_load(reinterpret_cast<const typename RopeVec<IO, V>::type*>(p));
   if constexpr (V == 1) {
-    x[0] = *p;
+    x[0] = to_f32(t);
   } else {
-    const f4 t = ld_nt(p);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = t[i];
-  }
-}
-template <int V> __device__ __forceinline__ void load_v(const __bf16* p, float* x) {
-  if constexpr (V == 1) {
-    x[0] = (float)*p;
-  } else {
-    Piece<__bf16> t;
-    t.load(p);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = t.at(i);
+    for (int i = 0; i < V; ++i) x[i] = to_f32(t[i]);
   }
 }
 template <int V, typename IO> __device__ __forceinline__ void store_v(IO* p, const float* x) {
+  typename RopeVec<IO, V>::type o;
   if constexpr (V == 1) {
-    *p = from_f32<IO>(x[0]);
+    o = from_f32<IO>(x[0]);
   } else {
-    typedef IO vec __attribute__((ext_vector_type(V)));
-    vec o;
 #pragma unroll
     for (int i = 0; i < V; ++i) o[i] = from_f32<IO>(x[i]);
-    *reinterpret_cast<vec*>(p) = o;
   }
+  *reinterpret_cast<typename RopeVec<IO, V>::type*>(p) = o;
 }
 
-// V: elements of a piece: 16 bytes where sizes, strides and pointers allow it,
-// else 1.  IL: interleaved pairs.
+// V: elements of a piece, up to 16 bytes: a power of two that divides the pairs'
+// runs and the copied rest.  IL: interleaved pairs.
+//
+// Units of the run, in order: token, head (queries before keys), then of a head
+// the pieces of pairs and those that are copied.  A thread takes one of every 256,
+// UB at a time: their loads are in flight together, and the first ones' while
+// the angles are formed.
 template <typename IO, int V, bool IL>
 __global__ void __launch_bounds__(256) rope_kernel(RopeParams p) {
   __shared__ float2 turn[kRopeAngles];  // factor * (cos, sin), [token][pair]
   __shared__ double at[kRopeRun];
   __shared__ int is_row[kRopeRun];
+  constexpr bool TWO = !(IL && V > 1);  // a unit of pairs is two pieces, or neighbours in one
+  constexpr int PAIRS = TWO ? V : V / 2, UB = TWO ? 2 : 4;
   const int64_t t0 = (int64_t)blockIdx.x * p.run;
   const int n = (int)min((int64_t)p.run, p.total - t0);
   const int half = p.rot / 2;
+  const uint32_t turned = half / PAIRS, per_head = turned + (p.d - p.rot) / V, heads = p.hq + p.hkv, per_tok = heads * per_head;
+  const uint32_t step_tok = 256 / per_tok, step_in = 256 - step_tok * per_tok, step_head = step_in / per_head,
+                 step_i = step_in - step_head * per_head;
+  uint32_t tok = threadIdx.x / per_tok, hh = (threadIdx.x - tok * per_tok) / per_head,
+           i = threadIdx.x - tok * per_tok - hh * per_head;
+
+  struct Unit { IO* dst; int tok, i; bool skip; float a[V], b[TWO ? V : 1]; } u[UB];
+  auto load = [&]() {
+#pragma unroll
+    for (int k = 0; k < UB; ++k) {
+      u[k].tok = tok;
+      u[k].i = i;
+      const bool is_k = hh >= (uint32_t)p.hq, copied = i >= turned;
+      u[k].skip = (int)tok >= n || (copied && !(is_k ? p.k_copy : p.q_copy));
+      if (!u[k].skip) {
+        const int h = is_k ? hh - p.hq : hh;
+        const int64_t t = t0 + tok;
+        const int e = copied ? p.rot + (i - turned) * V : IL ? i * (TWO ? 2 : V) : i * V;
+        const IO* src = (is_k ? (const IO*)p.k + t * p.k_st + h * p.k_sh : (const IO*)p.q + t * p.q_st + h * p.q_sh) + e;
+        u[k].dst = (is_k ? (IO*)p.ko + t * p.ko_st + h * p.ko_sh : (IO*)p.qo + t * p.qo_st + h * p.qo_sh) + e;
+        load_v<V>(src, u[k].a);
+        if constexpr (TWO)
+          if (!copied) load_v<V>(src + (IL ? 1 : half), u[k].b);
+      }
+      tok += step_tok;
+      hh += step_head;
+      i += step_i;
+      if (i >= per_head) {
+        i -= per_head;
+        ++hh;
+      }
+      if (hh >= heads) {
+        hh -= heads;
+        ++tok;
+      }
+    }
+  };
+  load();
+
   if ((int)threadIdx.x < n) {
     const int64_t i = t0 + threadIdx.x;
     bool ok = true;
@@ -96,56 +136,34 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeParams p) {
     turn[i] = make_float2(c * p.factor, s * p.factor);
   }
   __syncthreads();
-  // Units of the run: token, head (queries before keys), then of a head the
-  // pieces of pairs and those that are copied.
-  constexpr int PAIRS = IL && V > 1 ? V / 2 : V;  // pairs of a unit
-  const int turned = half / PAIRS, per_head = turned + (p.d - p.rot) / V, per_tok = (p.hq + p.hkv) * per_head;
-  auto load_or_zero = [](const IO* s, bool row, float* x) {
-    if (row) {
-      load_v<V>(s, x);
-    } else {
+  while (u[0].tok < n) {
 #pragma unroll
-      for (int k = 0; k < V; ++k) x[k] = 0.f;
+    for (int k = 0; k < UB; ++k) {
+      if (u[k].skip) continue;
+      const bool row = is_row[u[k].tok];
+      if (!row) {
+        if (!p.zero_rest) continue;
+#pragma unroll
+        for (int e = 0; e < V; ++e) u[k].a[e] = 0.f;
+        if constexpr (TWO)
+#pragma unroll
+          for (int e = 0; e < V; ++e) u[k].b[e] = 0.f;
+      }
+      if (u[k].i < (int)turned) {
+        const float2* w = turn + u[k].tok * half + u[k].i * PAIRS;
+#pragma unroll
+        for (int e = 0; e < PAIRS; ++e) {
+          float& x = u[k].a[TWO ? e : 2 * e];
+          float& y = TWO ? u[k].b[TWO ? e : 0] : u[k].a[TWO ? 0 : 2 * e + 1];
+          const float x0 = x, y0 = y, c = row ? w[e].x : 0.f, s = row ? w[e].y : 0.f;
+          x = x0 * c - y0 * s;
+          y = x0 * s + y0 * c;
+        }
+        if constexpr (TWO) store_v<V>(u[k].dst + (IL ? 1 : half), u[k].b);
+      }
+      store_v<V>(u[k].dst, u[k].a);
     }
-  };
-  for (int u = threadIdx.x; u < n * per_tok; u += 256) {
-    const int t = u / per_tok, r = u - t * per_tok, hh = r / per_head, i = r - hh * per_head;
-    const bool row = is_row[t];
-    if (!row && !p.zero_rest) continue;
-    const bool is_k = hh >= p.hq;
-    const int h = is_k ? hh - p.hq : hh;
-    const IO* src = is_k ? (const IO*)p.k + (t0 + t) * p.k_st + h * p.k_sh : (const IO*)p.q + (t0 + t) * p.q_st + h * p.q_sh;
-    IO* dst = is_k ? (IO*)p.ko + (t0 + t) * p.ko_st + h * p.ko_sh : (IO*)p.qo + (t0 + t) * p.qo_st + h * p.qo_sh;
-    float a[V], b[V];
-    if (i >= turned) {
-      if (is_k ? p.k_copy : p.q_copy) {
-        const int e = p.rot + (i - turned) * V;
-        load_or_zero(src + e, row, a);
-        store_v<V>(dst + e, a);
-      }
-    } else if constexpr (IL && V > 1) {
-      load_or_zero(src + i * V, row, a);
-#pragma unroll
-      for (int k = 0; k < PAIRS; ++k) {
-        const float2 w = turn[t * half + i * PAIRS + k];
-        b[2 * k] = a[2 * k] * w.x - a[2 * k + 1] * w.y;
-        b[2 * k + 1] = a[2 * k] * w.y + a[2 * k + 1] * w.x;
-      }
-      store_v<V>(dst + i * V, b);
-    } else {
-      const int e = IL ? 2 * i : i * V, f = IL ? e + 1 : e + half;
-      load_or_zero(src + e, row, a);
-      load_or_zero(src + f, row, b);
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const float2 w = turn[t * half + i * V + k];
-        const float x = a[k], y = b[k];
-        a[k] = x * w.x - y * w.y;
-        b[k] = x * w.y + y * w.x;
-      }
-      store_v<V>(dst + e, a);
-      store_v<V>(dst + f, b);
-    }
+    load();
   }
 }
 
@@ -153,6 +171,18 @@ template <typename IO, int V>
 static void launch_rope_v(const RopeParams& p, bool interleaved, dim3 grid, hipStream_t stream) {
   if (interleaved) hipLaunchKernelGGL((rope_kernel<IO, V, true>), grid, dim3(256), 0, stream, p);
   else hipLaunchKernelGGL((rope_kernel<IO, V, false>), grid, dim3(256), 0, stream, p);
+}
+template <typename IO>
+static void launch_rope_t(const RopeParams& p, int v, bool interleaved, dim3 grid, hipStream_t stream) {
+  if (v == 8) {
+    if constexpr (sizeof(IO) == 2) launch_rope_v<IO, 8>(p, interleaved, grid, stream);
+  } else if (v == 4) {
+    launch_rope_v<IO, 4>(p, interleaved, grid, stream);
+  } else if (v == 2) {
+    launch_rope_v<IO, 2>(p, interleaved, grid, stream);
+  } else {
+    launch_rope_v<IO, 1>(p, interleaved, grid, stream);
+  }
 }
 
 hipError_t launch_rope(const gdn_rope_args& a, hipStream_t stream) {
@@ -185,31 +215,24 @@ hipError_t launch_rope(const gdn_rope_args& a, hipStream_t stream) {
   p.rot = a.rot;
   p.q_copy = a.q != a.q_out;
   p.k_copy = a.k != a.k_out;
-  // Pieces of 16 bytes where every one of them is aligned.
-  const int es = a.io_dtype == GDN_BF16 ? 2 : 4, v = 16 / es;
-  const int64_t strides = a.q_stride_token | a.q_stride_head | a.qo_stride_token | a.qo_stride_head |
-                          (a.k ? a.k_stride_token | a.k_stride_head | a.ko_stride_token | a.ko_stride_head : 0);
-  const uintptr_t bases = (uintptr_t)a.q | (uintptr_t)a.q_out | (a.k ? (uintptr_t)a.k | (uintptr_t)a.k_out : 0);
-  const int step = a.interleaved ? a.rot : a.rot / 2;
-  const bool vec = strides % v == 0 && bases % 16 == 0 && a.d % v == 0 && step % v == 0;
-  // Tokens per workgroup: as many as their angles' room holds and about 4096
-  // pieces, but at least 1024 workgroups before one takes a second token.
-  const int64_t pieces = (int64_t)(p.hq + p.hkv) * (vec ? a.d / v : a.d);
-  const int64_t room = kRopeAngles / (a.rot / 2);
-  int64_t run = 4096 / pieces, most = a.total_tokens / 1024;
+  const bool interleaved = a.interleaved != 0;
+  int v = a.io_dtype == GDN_BF16 ? 8 : 4;
+  while (((interleaved ? a.rot : a.rot / 2) | (a.d - a.rot)) % v != 0) v /= 2;
+  // Tokens per workgroup: about two rounds of what its threads hold (32768 tokens of 40
+  // heads of 128, bf16: four tokens 126 us, one 143, eight 132), within the angles'
+  // room, but at least 1024 workgroups before one takes a second token.
+  const bool two = !interleaved || v == 1;
+  const int64_t units = (int64_t)(p.hq + p.hkv) * (two ? a.rot / 2 / v + (a.d - a.rot) / v : a.d / v);
+  const int64_t room = kRopeAngles / (a.rot / 2), round = two ? 512 : 1024;
+  int64_t run = (2 * round + units / 2) / units, most = a.total_tokens / 1024;
   run = run > most ? most : run;
   run = run > kRopeRun ? kRopeRun : run;
   run = run > room ? room : run < 1 ? 1 : run;
   if (a.total_tokens / run > (1 << 23)) run = 2;  // a grid's limit; total_tokens <= 2^24, and there is room for two
   p.run = (int)run;
   const dim3 grid((unsigned)((a.total_tokens + run - 1) / run));
-  if (es == 2) {
-    if (vec) launch_rope_v<__bf16, 8>(p, a.interleaved != 0, grid, stream);
-    else launch_rope_v<__bf16, 1>(p, a.interleaved != 0, grid, stream);
-  } else {
-    if (vec) launch_rope_v<float, 4>(p, a.interleaved != 0, grid, stream);
-    else launch_rope_v<float, 1>(p, a.interleaved != 0, grid, stream);
-  }
+  if (a.io_dtype == GDN_BF16) launch_rope_t<__bf16>(p, v, interleaved, grid, stream);
+  else launch_rope_t<float>(p, v, interleaved, grid, stream);
   return hipGetLastError();
 }
 
