@@ -139,6 +139,7 @@ class PagesArgs(ctypes.Structure):
 
 _lock = threading.Lock()
 _lib = None
+_calls = None
 
 
 def load(path: str | None = None):
@@ -194,6 +195,20 @@ def load(path: str | None = None):
         if path is None:
             _lib = lib
         return lib
+
+
+def calls():
+    """The module _calls (binding/calls.cpp), bound to the library."""
+    global _calls
+    if _calls is None:
+        lib = load()
+        if not os.path.exists(os.path.join(PKG, "_calls.so")):
+            raise RuntimeError("_calls.so is not built; run `python -m gated_deltanet_state_delta_amd.build`")
+        from . import _calls as module
+        module.bind(*(ctypes.cast(getattr(lib, "gdn_" + name), _vp).value for name in
+                      ("attn_decode", "attn_decode_workspace_size", "kv_append", "kv_read", "rope")))
+        _calls = module
+    return _calls
 
 
 class GdnError(RuntimeError):

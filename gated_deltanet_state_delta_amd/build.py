@@ -1,8 +1,9 @@
-"""Build libgdn.so (HIP, gfx950) in-tree.
+"""Build libgdn.so (HIP, gfx950) and the binding's _calls.so in-tree.
 
 Every translation unit under csrc/ is compiled with hipcc for gfx950 into
 _build/, in parallel, and linked into gated_deltanet_state_delta_amd/libgdn.so.
-Packed-fp32 VALU instructions are disabled for all device code.
+Packed-fp32 VALU instructions are disabled for all device code.  Beside it,
+binding/calls.cpp (host code only) becomes the CPython module _calls.
 
     python -m gated_deltanet_state_delta_amd.build [--jobs N]
 """
@@ -20,6 +21,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build", "libgdn")
 LIB = os.path.join(PKG, "libgdn.so")
+CALLS = os.path.join(PKG, "_calls.so")
 ARCH = "gfx950"
 
 DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
@@ -75,12 +77,36 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_calls() -> str:
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    tmp = CALLS + ".tmp%d" % os.getpid()
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI]
+    for d in cpp_extension.include_paths() + [sysconfig.get_paths()["include"]]:
+        cmd += ["-isystem", d]
+    # torch's libraries are loaded before the module, so it carries no path to them
+    cmd += [os.path.join(PKG, "binding", "calls.cpp"), "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"),
+            "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", tmp]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed for binding/calls.cpp:\n" + res.stderr)
+    if res.stderr.strip():
+        sys.stderr.write(res.stderr)
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 def build(jobs: int | None = None) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
     jobs = jobs or min(len(srcs), max(1, min(16, os.cpu_count() or 1)))
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+        calls = ex.submit(_build_calls)
         objs = list(ex.map(_compile, srcs))
+        calls.result()
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [hipcc(), "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp] + objs
     res = subprocess.run(cmd, capture_output=True, text=True)

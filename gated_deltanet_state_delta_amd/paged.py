@@ -25,7 +25,14 @@ from . import _lib
 _I32_MIN, _I32_MAX = -(1 << 31), (1 << 31) - 1
 _IO = {torch.float32: _lib.GDN_F32, torch.bfloat16: _lib.GDN_BF16}
 _CACHE = {**_IO, torch.float8_e4m3fn: _lib.GDN_E4M3, torch.int8: _lib.GDN_I8}
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
+def _short(name, *args):
+    """The call by the short way (binding/calls.cpp) on the current device and
+    stream, or None where it is not an ordinary one."""
+    dev = _current_device()
+    return getattr(_lib._calls or _lib.calls(), name)(*args, dev, _raw_stream(dev))
 
 
 def _on(stream, dev, tensors):
@@ -225,6 +232,10 @@ def attn_decode(q, k_cache, v_cache, page_table, lens, *, scale=None, k_scale=No
     attn_decode_workspace_size bytes for the split over the rows' lengths;
     None allocates one.  Returns out [B, T, hq, d] in q's dtype.
     """
+    if out is None and workspace is None and stream is None and not return_lse and q.is_cuda:
+        got = _short("attn_decode", q, k_cache, v_cache, page_table, lens, scale, k_scale, v_scale)
+        if got is not None:
+            return got
     dev = q.device
     ctx = _on(stream, dev, (k_cache, v_cache, page_table, lens, k_scale, v_scale, out, workspace))
     if ctx is not None:
@@ -324,6 +335,9 @@ def kv_append(k, v, k_cache, v_cache, page_table, lens, *, cu_seqlens=None, k_sc
     slot of a block starts it anew, so pages need no clearing.  NaN in a token
     makes the scale of an int8 block NaN.  Returns (k_cache, v_cache).
     """
+    if stream is None and k.is_cuda:
+        if _short("kv_append", k, v, k_cache, v_cache, page_table, lens, cu_seqlens, k_scale, v_scale):
+            return k_cache, v_cache
     dev = k.device
     ctx = _on(stream, dev, (v, k_cache, v_cache, page_table, lens, cu_seqlens, k_scale, v_scale))
     if ctx is not None:
@@ -391,6 +405,11 @@ def kv_read(k_cache, v_cache, page_table, lens, tokens, *, cu_seqlens=None, dtyp
     out: (k, v) to write to; tokens of no row are left as they were there, and
     zeros in new ones.  Returns (k, v): [B, tokens, hkv, d], or [tokens, hkv, d].
     """
+    if out is None and stream is None and k_cache.is_cuda:
+        io = _IO.get(dtype or k_cache.dtype, _lib.GDN_BF16 if dtype is None else -1)
+        got = _short("kv_read", k_cache, v_cache, page_table, lens, tokens, cu_seqlens, io, k_scale, v_scale)
+        if got is not None:
+            return got
     dev = k_cache.device
     ctx = _on(stream, dev, (v_cache, page_table, lens, cu_seqlens, k_scale, v_scale) + tuple(out or ()))
     if ctx is not None:

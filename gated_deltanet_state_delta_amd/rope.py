@@ -14,7 +14,7 @@ from ctypes import byref
 import torch
 
 from . import _lib
-from .paged import _IO, _checked, _i32, _library, _on, _ptr, _raw_stream
+from .paged import _IO, _checked, _i32, _library, _on, _ptr, _raw_stream, _short
 
 
 def rope_frequencies(rot, *, base=10000.0, scaling=None, scale=1.0, trained=None, slow=1.0, fast=32.0, device=None):
@@ -152,6 +152,10 @@ def rope(q, k, inv_freq, *, lens=None, cu_seqlens=None, positions=None, interlea
     Packed tokens of no row are left as they were there, and zeros in new ones.
     Returns (q, k).
     """
+    if out is None and stream is None and q.is_cuda:
+        got = _short("rope", q, k, inv_freq, lens, cu_seqlens, positions, interleaved, factor)
+        if got is not None:
+            return got
     dev = q.device
     ctx = _on(stream, dev, (k, inv_freq, lens, cu_seqlens, positions) + tuple(out or ()))
     if ctx is not None:
