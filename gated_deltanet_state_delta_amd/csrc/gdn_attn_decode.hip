@@ -115,7 +115,7 @@ static int attn_tiles(const gdn_attn_decode_args& a) {
   return (R + rows - 1) / rows;
 }
 static int attn_shares(const gdn_attn_decode_args& a) {
-  const int es = cache_bytes(a.cache_dtype), tile = attn_tile(es, a.d);
+  const int es = cache_bytes(a.cache_dtype), tile = attn_tile(es, a.d, a.scale_block > 0);
   const int64_t cap = (int64_t)a.max_pages * a.page_size, steps = a.batch * ((cap + tile - 1) / tile);
   const int alone = tile < 32 ? 64 : 128;
   if (cap <= alone || a.batch > kMostRows || (int64_t)a.batch * a.hq * a.T > (1 << 24)) return 0;
@@ -125,8 +125,20 @@ static int attn_shares(const gdn_attn_decode_args& a) {
   return n < 2 ? 0 : (int)n;
 }
 
+// Instead of shares and the second launch, for short tables of block-scaled
+// caches: the four waves of a workgroup take a quarter each of a row, head and
+// row tile, and join in LDS.  From 64 tokens, where one wave does as well, to 512,
+// while two such workgroups a CU hold everything at a time or two (8 heads of 128,
+// bf16 over e4m3: 1 row of 256 tokens 7.3 us against 10.3, of 512 9.6 against
+// 11.0, of 1024 16 against 11; 64 rows of 256 12.6 against 17, of 512 19 against
+// 23; 256 rows of 256 35 against 30).
+static bool attn_team(const gdn_attn_decode_args& a) {
+  const int64_t cap = (int64_t)a.max_pages * a.page_size;
+  return a.scale_block > 0 && cap > 64 && cap <= 512 && (int64_t)a.batch * a.hkv * attn_tiles(a) <= 1024;
+}
+
 size_t attn_workspace_bytes(const gdn_attn_decode_args& a) {
-  if (a.batch == 0 || a.max_pages == 0) return 0;
+  if (a.batch == 0 || a.max_pages == 0 || attn_team(a)) return 0;
   const int shares = attn_shares(a);
   if (shares == 0) return 0;
   return (2 * (size_t)shares * a.hq * a.T * (a.d + 2) + 2 * (size_t)a.batch) * sizeof(float);
@@ -166,6 +178,8 @@ hipError_t launch_attn_decode(const gdn_attn_decode_args& a, hipStream_t stream)
   p.v_scale = a.v_scale;
   p.k_blocks = a.k_block_scale;
   p.v_blocks = a.v_block_scale;
+  p.block = a.scale_block;
+  p.blk_sp = a.scale_block > 0 ? (int64_t)a.hkv * (a.page_size / a.scale_block) : 0;
   p.nblk = a.scale_block > 0 ? a.page_size / a.scale_block : 0;
   p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
   p.batch = a.batch;
@@ -181,6 +195,7 @@ hipError_t launch_attn_decode(const gdn_attn_decode_args& a, hipStream_t stream)
   divider(a.page_size, p.page_mul, p.page_shift);
   divider(a.scale_block > 0 ? a.scale_block : 1, p.blk_mul, p.blk_shift);
   const size_t need = attn_workspace_bytes(a);
+  p.team = attn_team(a);
   p.shares = a.batch;
   p.plan = nullptr;
   p.part_o = p.part_ml = nullptr;
@@ -194,7 +209,7 @@ hipError_t launch_attn_decode(const gdn_attn_decode_args& a, hipStream_t stream)
   // Workgroups of 4 waves: see the kernel's mapping.
   const int rtw = p.ntile > 2 ? 4 : p.ntile, nwg = (p.ntile + rtw - 1) / rtw, per = 8 * (4 / rtw);
   const int64_t units = (int64_t)p.shares * p.hkv;
-  const dim3 grid((unsigned)((units + per - 1) / per * 8 * nwg));
+  const dim3 grid((unsigned)(p.team ? (units + 7) / 8 * 8 * p.ntile : (units + per - 1) / per * 8 * nwg));
   hipError_t e;
   if (a.cache_dtype == GDN_I8)  // block scales always
     e = a.io_dtype == GDN_BF16 ? launch_attn_bf16_i8_blocks(p, a.d, grid, stream) : launch_attn_f32_i8_blocks(p, a.d, grid, stream);

@@ -42,9 +42,16 @@
 
 namespace gdn {
 
-// BS: block scales.  A tile's are read one tile ahead, a key by each lane, and
-// go through LDS to the lanes that hold the key's scores: the key's factor
-// enters the score, the value's the weight before the product.
+// Block scales: a key's factor enters its score, a value's the weight before
+// the product.  A lane holds four neighbouring keys' scores.
+//  * kBlocksWide: blocks of 4, 8 or a multiple of 16 tokens, pages of a multiple
+//    of 16: one factor for the four, loaded where it is (the subtile's first
+//    factor through a scalar, the lane's own at a fixed offset from there);
+//  * kBlocksOne: blocks of one token: four factors, likewise;
+//  * kBlocksAny: other sizes: read a tile ahead, a key by each lane, and passed
+//    through LDS.
+constexpr int kBlocksNone = 0, kBlocksWide = 1, kBlocksOne = 2, kBlocksAny = 3;
+
 struct AttnParams {
   const void* q;
   int64_t q_sb, q_st, q_sh;  // bytes
@@ -63,13 +70,15 @@ struct AttnParams {
   const float* k_blocks;  // block scales, [n_pages][hkv][nblk]
   const float* v_blocks;
   uint32_t blk_mul, blk_shift;  // j / scale_block, as j / page_size below
-  int nblk;
+  int block, nblk;
+  int64_t blk_sp;  // scales of a page
   float* part_o;   // [2 * shares][hkv][R][D]; the workspace's arrays are null when each row is one share
   float* part_ml;  // [2 * shares][hkv][R][2]
   int2* plan;      // [batch]: a row's first share and how many it lies in
   float scale_log2;
   uint32_t page_mul, page_shift;  // j / page_size = (j * page_mul) >> page_shift
   int batch, T, hq, hkv, group, R, ntile, n_pages, page_size, cap, shares;
+  int team;        // BS: a workgroup's waves share a row, head and row tile, and join in LDS
 };
 
 __device__ __forceinline__ int attn_len(const AttnParams& p, int b) {
@@ -203,6 +212,15 @@ __device__ __forceinline__ uint32_t bf_pair(const Raw<N>& r, int i) {
   } else return __builtin_bit_cast(uint32_t, (i & 1) ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r.w[i >> 1], 1.0f, true)
                                                    : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r.w[i >> 1], 1.0f, false));
 }
+// A value at a uniform address that nothing writes during the kernel, through the scalar cache.
+template <typename T> __device__ __forceinline__ T load_const(const T* p) {
+  return *(const __attribute__((address_space(4))) T*)(uintptr_t)p;
+}
+// A pointer that is the same in all lanes, in scalar registers.
+template <typename T> __device__ __forceinline__ const T* uniform_ptr(const T* p) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)(uint64_t)p), hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)p >> 32));
+  return (const T*)((uint64_t)hi << 32 | lo);
+}
 // Elements 2i and 2i+1 of an fp32 piece.
 template <int N>
 __device__ __forceinline__ f2 f_pair(const Raw<N>& r, int i) {
@@ -237,6 +255,8 @@ __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2
 // heads of 128, bf16: 172 us; two waves of 4 KiB 175, two of 8 KiB 184, three
 // 193).  Shorter rows, and e4m3 whose conversion is VALU work: two waves, 4
 // KiB (256 rows, 2 heads of 256, e4m3: 110 us; one wave 131, three 122).
+// With block scales heads of 64 and fewer take 2 KiB (64 ragged rows up to 8192
+// tokens, 16 heads of 64, int8: 140 us, 4 KiB 159; heads of 128 gain 2% or lose 5%).
 constexpr int attn_occ(int es, int d) { return es > 1 && d >= 128 ? 1 : 2; }
 
 // IO: type of q and out; KE: cache element.  The products are bf16, or fp32
@@ -258,12 +278,12 @@ constexpr int attn_rows16(int kind, int d, int io) { return kind < 2 || (io == 4
 constexpr int attn_waves(int es, int d, int kind) { return kind > 1 ? d > 64 ? 1 : 2 : attn_occ(es, d); }
 
 // Keys of a wave's tile, a multiple of the products' depth.
-constexpr int attn_tile(int es, int d) {
-  const int keys = 8192 / attn_occ(es, d) / (d * es);
+constexpr int attn_tile(int es, int d, bool bs) {
+  const int keys = (bs && d <= 64 ? 2048 : 8192 / attn_occ(es, d)) / (d * es);
   return keys > 64 ? 64 : keys < 16 ? 16 : keys;
 }
 
-template <typename IO, typename KE, int D, int KIND>
+template <typename IO, typename KE, int D, int KIND, bool BS>
 struct AttnCfg {
   static constexpr int ES = sizeof(KE);
   static constexpr bool BF = ES < 4;
@@ -271,7 +291,7 @@ struct AttnCfg {
   static constexpr int kmin(int a, int b) { return a < b ? a : b; }
   static constexpr int KW = kmin(16 / ES, D / 4), NC = D / (4 * KW);    // elements per K piece, pieces per row and lane
   static constexpr int VW = kmin(16 / ES, D / 16), U = D / (16 * VW);   // the same for V
-  static constexpr int OCC = attn_waves(ES, D, KIND), KT = attn_tile(ES, D);
+  static constexpr int OCC = attn_waves(ES, D, KIND), KT = attn_tile(ES, D, BS);
   static constexpr int NT = KT / 16;
   static constexpr int NA = D / 16;  // accumulator tiles
 };
@@ -280,9 +300,9 @@ struct AttnCfg {
 // page: its base is a scalar and rows past the end read zeros through the
 // buffer's bound.  Otherwise each key's offset is looked up by one lane and
 // passed through LDS.
-template <typename IO, typename KE, int D, bool UNI, int KIND, bool BS>
-__global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND>::OCC)) attn_decode_kernel(AttnParams p) {
-  typedef AttnCfg<IO, KE, D, KIND> C;
+template <typename IO, typename KE, int D, bool UNI, int KIND, int BS>
+__global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND, BS != kBlocksNone>::OCC)) attn_decode_kernel(AttnParams p) {
+  typedef AttnCfg<IO, KE, D, KIND, BS != kBlocksNone> C;
   constexpr int KT = C::KT, NT = C::NT, NC = C::NC, KW = C::KW, VW = C::VW, U = C::U, NA = C::NA, ES = C::ES;
   constexpr int QT = C::QT, PT = C::PT, RT = attn_rows16(KIND, D, sizeof(IO));
   // Where no second wave reads a key, non-temporal loads leave the caches
@@ -291,7 +311,7 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND>::OCC)) attn_dec
   constexpr bool BF = C::BF, MT = KIND > 0, ONCE = KIND < 2 || (KIND == 2 && RT == 2);
   constexpr uint64_t kNone = ~0ull;
   __shared__ uint64_t offs[UNI ? 1 : 4][2][2][UNI ? 1 : KT];  // [wave][parity][K, V][key]
-  __shared__ __align__(16) float blocks[BS ? 4 : 1][2][BS ? KT : 4];  // [wave][K, V][key]: a tile's scales
+  __shared__ __align__(16) float blocks[BS == kBlocksAny ? 4 : 1][2][BS == kBlocksAny ? KT : 4];  // [wave][K, V][key]: a tile's scales
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -301,23 +321,29 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND>::OCC)) attn_dec
   // further workgroups of one (share, head) are 8 apart and so on one XCD
   // (workgroups go round the 8).
   const int rtw = p.ntile > 2 ? 4 : p.ntile, nwg = (p.ntile + rtw - 1) / rtw;
-  const int unit = (int)((blockIdx.x / (8 * nwg) * 8 + (blockIdx.x & 7)) * (4 / rtw)) + wave / rtw;
-  const int rt = (int)(blockIdx.x / 8 % nwg) * rtw + wave % rtw;
+  const bool team = BS != kBlocksNone && p.team;
+  const int unit = team ? (int)(blockIdx.x / (8 * p.ntile) * 8 + (blockIdx.x & 7))
+                        : (int)((blockIdx.x / (8 * nwg) * 8 + (blockIdx.x & 7)) * (4 / rtw)) + wave / rtw;
+  const int rt = team ? (int)(blockIdx.x / 8 % p.ntile) : (int)(blockIdx.x / 8 % nwg) * rtw + wave % rtw;
   const int h = unit % p.hkv, share_id = unit / p.hkv;
   if (share_id >= p.shares || rt >= p.ntile) return;
-  AttnShare share = attn_share<KT>(p, share_id, lane);
+  AttnShare share = attn_share<KT>(p, share_id, lane);  // (team: the row)
+  // Uniform values that come from loads, into scalar registers: the walk's addresses follow from them.
+  auto uniform = [](int v) { return BS != kBlocksNone ? __builtin_amdgcn_readfirstlane(v) : v; };
+  share.n = uniform(share.n);
 
-  const float s_scale = BS ? p.scale_log2 : p.scale_log2 * (p.k_scale ? p.k_scale[h] : 1.0f);
+  const float s_scale = BS != kBlocksNone ? p.scale_log2 : p.scale_log2 * (p.k_scale ? p.k_scale[h] : 1.0f);
 
   while (share.n > 0) {
-    const int b = share.b, len = attn_len(p, b), row_steps = attn_steps<KT>(len), at = share.at;
-    const int take = min(share.n, row_steps - at);
+    const int b = uniform(share.b), len = uniform(attn_len(p, b)), row_steps = attn_steps<KT>(len), part = (row_steps + 3) >> 2;
+    const int at = team ? min(wave * part, row_steps) : uniform(share.at);
+    const int take = min(team ? part : share.n, row_steps - at);
     const int c0 = at * KT, c1 = min(len, (at + take) * KT);
-    const bool whole = take == row_steps;
+    const bool whole = take == row_steps || team;
     const int slot = 2 * share_id + (at == 0);  // of a part: one that begins a row, one that does not
     if (p.plan && at == 0 && h == 0 && rt == 0 && lane == 0)
       p.plan[b] = make_int2(share_id, 1 + (row_steps - take + share.size - 1) / share.size);
-    share.n -= take;
+    share.n = team ? 0 : share.n - take;
     share.b = b + 1;
     share.at = 0;
 
@@ -374,6 +400,7 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND>::OCC)) attn_dec
     const char* kbase = (const char*)p.k + h * p.k_sh;
     const char* vbase = (const char*)p.v + h * p.v_sh;
     const int32_t* tab = p.table + b * p.table_stride;
+    if constexpr (BS != kBlocksNone) tab = uniform_ptr(tab);
 
     f4 acc[RT][NA];
     float m[RT], l[RT];
@@ -396,7 +423,10 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND>::OCC)) attn_dec
     auto load_ents = [&](int key0) {
       Ents o;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) o.e[n] = tab[page_of(min(key0 + 16 * n, len - 1))];
+      for (int n = 0; n < NT; ++n) {
+        const int at = page_of(min(key0 + 16 * n, len - 1));
+        o.e[n] = BS != kBlocksNone ? load_const(tab + at) : tab[at];
+      }
       return o;
     };
     // UNI: the resource of one subtile's rows of K or V: `rows` valid rows
@@ -408,18 +438,51 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND>::OCC)) attn_dec
       const uint32_t bytes = rows > 0 ? (uint32_t)(rows - 1) * st + D * ES : 0u;
       return buf_rsrc_n(base + (ok ? (int64_t)ent * sp : 0) + (int64_t)off * st, bytes);
     };
-    auto issue_k_uni = [&](const Ents& en, int key0) {
+    // The factors of the lane's keys in one subtile (kBlocksWide: one).
+    constexpr bool LANE = BS == kBlocksWide || BS == kBlocksOne;
+    typedef float Four __attribute__((ext_vector_type(BS == kBlocksOne ? 4 : 1), aligned(4)));
+    const int fac_at = BS == kBlocksOne ? 4 * g : p.block >= 16 ? 0 : p.block == 8 ? g >> 1 : g;
+    const float* kfac = p.k_blocks + (int64_t)h * p.nblk;
+    const float* vfac = p.v_blocks + (int64_t)h * p.nblk;
+    // LANE: what K's and V's loads of a subtile share, found a tile ahead for K.
+    struct Sub { int ent, off, blk, rows; bool ok; };  // entry (0 where there is none), first slot, its block, rows that exist
+    struct Subs { Sub s[LANE ? NT : 1]; } sub_cur = {}, sub_next = {};
+    auto find_subs = [&](const Ents& en, int key0) {
+      Subs o = {};
+#pragma unroll
+      for (int n = 0; n < (LANE ? NT : 0); ++n) {
+        Sub& s = o.s[n];
+        const int key = key0 + 16 * n;
+        s.ok = en.e[n] >= 0 && en.e[n] < p.n_pages;
+        s.ent = s.ok ? en.e[n] : 0;
+        s.off = key - page_of(key) * p.page_size;
+        s.blk = (int)(((uint64_t)(uint32_t)s.off * p.blk_mul) >> p.blk_shift);
+        s.rows = s.ok && key < c1 ? min(16, len - key) : 0;
+      }
+      return o;
+    };
+    auto rows_of = [&](const char* base, int64_t sp, uint32_t st, const Sub& s) {
+      return buf_rsrc_n(base + s.ent * sp + (int64_t)s.off * st, s.rows > 0 ? (uint32_t)(s.rows - 1) * st + D * ES : 0u);
+    };
+    auto load_factors = [&](const float* base, const Sub& s) {
+      return *reinterpret_cast<const Four*>(base + s.ent * p.blk_sp + s.blk + fac_at);
+    };
+    auto factor_of = [&](const Four& f, int j) { return f[BS == kBlocksOne ? j : 0]; };
+    Four kf[LANE ? NT : 1], vf[LANE ? NT : 1];
+    auto issue_k_uni = [&](const Ents& en, const Subs& su, int key0) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const auto rs = sub_rsrc(kbase, p.k_sp, p.k_st, en.e[n], key0 + 16 * n);
+        if constexpr (LANE) kf[n] = load_factors(kfac, su.s[n]);
+        const auto rs = LANE ? rows_of(kbase, p.k_sp, p.k_st, su.s[LANE ? n : 0]) : sub_rsrc(kbase, p.k_sp, p.k_st, en.e[n], key0 + 16 * n);
 #pragma unroll
         for (int c = 0; c < NC; ++c) kr[n][c] = raw_buf<KW * ES, ONCE>(rs, x * p.k_st + (4 * KW * c + KW * g) * ES);
       }
     };
-    auto issue_v_uni = [&](const Ents& en, int key0) {
+    auto issue_v_uni = [&](const Ents& en, const Subs& su, int key0) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const auto rs = sub_rsrc(vbase, p.v_sp, p.v_st, en.e[n], key0 + 16 * n);
+        if constexpr (LANE) vf[n] = load_factors(vfac, su.s[n]);
+        const auto rs = LANE ? rows_of(vbase, p.v_sp, p.v_st, su.s[LANE ? n : 0]) : sub_rsrc(vbase, p.v_sp, p.v_st, en.e[n], key0 + 16 * n);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -464,24 +527,17 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND>::OCC)) attn_dec
         }
     };
 
-    // The block scales of a tile, lane l's those of key l: 0 where no key is held.
+    // kBlocksAny: the factors of a tile, lane l's those of key l: 0 where no key is held.
     struct Scales { float k, v; };
     auto load_scales = [&](int ent, int key0) {
       const int key = key0 + lane;
       Scales o = {0.f, 0.f};
       if (lane < KT && key < len && ent >= 0 && ent < p.n_pages) {
         const int blk = (int)(((uint64_t)(uint32_t)key * p.blk_mul) >> p.blk_shift) - page_of(key) * p.nblk;
-        const int64_t at = ((int64_t)ent * p.hkv + h) * p.nblk + blk;
-        o.k = p.k_blocks[at];
-        o.v = p.v_blocks[at];
+        o.k = kfac[ent * p.blk_sp + blk];
+        o.v = vfac[ent * p.blk_sp + blk];
       }
       return o;
-    };
-    auto lane_ent = [&](const Ents& en) {  // UNI: the entry of key `lane`
-      int e = en.e[0];
-#pragma unroll
-      for (int n = 1; n < NT; ++n) e = lane >> 4 == n ? en.e[n] : e;
-      return e;
     };
 
     Ents ent_cur = {}, ent_next = {};
@@ -491,19 +547,19 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND>::OCC)) attn_dec
     if (c0 < c1) {
       if constexpr (UNI) {
         ent_cur = load_ents(c0);
-        issue_k_uni(ent_cur, c0);
-        if constexpr (BS) sc = load_scales(lane_ent(ent_cur), c0);
+        sub_cur = find_subs(ent_cur, c0);
+        issue_k_uni(ent_cur, sub_cur, c0);
         ent_next = load_ents(c0 + KT);
       } else {
         const int ent1 = load_ent1(c0);
         publish(ent1, c0, 0);
         issue_k_any(0);
-        if constexpr (BS) sc = load_scales(ent1, c0);
+        if constexpr (BS == kBlocksAny) sc = load_scales(ent1, c0);
         ent1_next = load_ent1(c0 + KT);
       }
     }
     for (int key0 = c0; key0 < c1; key0 += KT) {
-      if constexpr (UNI) issue_v_uni(ent_cur, key0);
+      if constexpr (UNI) issue_v_uni(ent_cur, sub_cur, key0);
       else issue_v_any(par);
 
       // ---- scores of the tile
@@ -540,8 +596,19 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND>::OCC)) attn_dec
           }
         }
       }
-      f4 ks[BS ? NT : 1], vs[BS ? NT : 1];  // of the lane's keys
-      if constexpr (BS) {
+      if constexpr (LANE) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float f = factor_of(kf[n], j) * s_scale;
+#pragma unroll
+            for (int q = 0; q < RT; ++q) s[q][n][j] *= f;
+          }
+        }
+      }
+      f4 ks[BS == kBlocksAny ? NT : 1], vs[BS == kBlocksAny ? NT : 1];  // of the lane's keys
+      if constexpr (BS == kBlocksAny) {
         __builtin_amdgcn_wave_barrier();
         if (lane < KT) {
           blocks[wave][0][lane] = sc.k * s_scale;
@@ -559,36 +626,49 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND>::OCC)) attn_dec
       if constexpr (UNI) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-          if (ent_cur.e[n] < 0 || ent_cur.e[n] >= p.n_pages) sub_ok &= ~(1u << n);
-        if (key0 + KT < c1) {
-          issue_k_uni(ent_next, key0 + KT);
-          if constexpr (BS) sc = load_scales(lane_ent(ent_next), key0 + KT);
-        }
+          if (LANE ? !sub_cur.s[LANE ? n : 0].ok : ent_cur.e[n] < 0 || ent_cur.e[n] >= p.n_pages) sub_ok &= ~(1u << n);
+        if constexpr (LANE) sub_next = find_subs(ent_next, key0 + KT);
+        // LANE: always, with no rows past the end, so that the values' wait need not count these loads in
+        if (LANE || key0 + KT < c1) issue_k_uni(ent_next, sub_next, key0 + KT);
+        sub_cur = sub_next;
         ent_cur = ent_next;
         ent_next = load_ents(key0 + 2 * KT);
       } else {
         par ^= 1;
-        if (key0 + KT < c1) {
+        if (BS != kBlocksNone || key0 + KT < c1) {
           publish(ent1_next, key0 + KT, par);
           issue_k_any(par);
-          if constexpr (BS) sc = load_scales(ent1_next, key0 + KT);
+          if constexpr (BS == kBlocksAny) sc = load_scales(ent1_next, key0 + KT);
           ent1_next = load_ent1(key0 + 2 * KT);
         }
       }
 
       // ---- masks, running maximum, weights
+      // all: every row of the wave sees every key of the tile.
+      const bool all = BS != kBlocksNone && key0 + KT <= len - p.T + 1 &&
+                       (UNI ? sub_ok == ~0u : __all((held & (~0u >> (32 - 4 * NT))) == ~0u >> (32 - 4 * NT)));
 #pragma unroll
       for (int q = 0; q < RT; ++q) {
         float mx = m[q];
+        if (all) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int key = key0 + 16 * n + 4 * g + j;
-            const bool sees = key < lim[q] && (UNI ? ((sub_ok >> n) & 1) != 0 : ((held >> (4 * n + j)) & 1) != 0);
-            s[q][n][j] = sees ? s[q][n][j] * (BS ? ks[BS ? n : 0][j] : s_scale) : -__builtin_inff();
-            mx = fmaxf(mx, s[q][n][j]);
-          }
+            for (int j = 0; j < 4; ++j) {
+              if constexpr (!LANE) s[q][n][j] *= ks[BS == kBlocksAny ? n : 0][j];
+              mx = fmaxf(mx, s[q][n][j]);
+            }
+        } else {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int key = key0 + 16 * n + 4 * g + j;
+              const bool sees = key < lim[q] && (UNI ? ((sub_ok >> n) & 1) != 0 : ((held >> (4 * n + j)) & 1) != 0);
+              s[q][n][j] = !sees ? -__builtin_inff() : LANE ? s[q][n][j] : s[q][n][j] * (BS == kBlocksAny ? ks[BS == kBlocksAny ? n : 0][j] : s_scale);
+              mx = fmaxf(mx, s[q][n][j]);
+            }
+        }
         mx = max_over_g(mx);
         const float mu = mx == -__builtin_inff() ? 0.f : mx;
         const float alpha = exp2_hw(m[q] - mu);
@@ -606,10 +686,25 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND>::OCC)) attn_dec
           for (int j = 0; j < 4; ++j) {
             s[q][n][j] = exp2_hw(s[q][n][j] - mu);
             l[q] += s[q][n][j];
-            // a key that another of the new tokens sees may have a scale that is not finite
-            if constexpr (BS)
-              s[q][n][j] = !MT || key0 + 16 * n + 4 * g + j < lim[q] ? s[q][n][j] * vs[BS ? n : 0][j] : 0.f;
           }
+        if constexpr (BS != kBlocksNone) {
+          auto vf_of = [&](int n, int j) { return LANE ? factor_of(vf[LANE ? n : 0], j) : vs[LANE ? 0 : n][j]; };
+          if (all) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) s[q][n][j] *= vf_of(n, j);
+          } else {  // a factor of a key that is not seen may be anything
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const bool sees = key0 + 16 * n + 4 * g + j < lim[q] &&
+                                  (UNI ? ((sub_ok >> n) & 1) != 0 : ((held >> (4 * n + j)) & 1) != 0);
+                s[q][n][j] = sees ? s[q][n][j] * vf_of(n, j) : 0.f;
+              }
+          }
+        }
       }
       if constexpr (!UNI) {  // a row that is not there must not reach the product
 #pragma unroll
@@ -756,6 +851,48 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND>::OCC)) attn_dec
       }
     }
 
+    if constexpr (BS != kBlocksNone) {
+      if (team) {
+        // The upper half of the waves hand what they have to the lower half, and so
+        // on down to wave 0, which writes the results: lane by lane, since a lane
+        // holds the same rows and dimensions in all of them.
+        __shared__ float parts[2][RT * (NA * 4 + 2)][64];
+#pragma unroll
+        for (int to = 2; to >= 1; to >>= 1) {
+          if (wave >= to && wave < 2 * to) {
+            int i = 0;
+#pragma unroll
+            for (int q = 0; q < RT; ++q) {
+              parts[wave - to][i++][lane] = m[q];
+              parts[wave - to][i++][lane] = l[q];
+#pragma unroll
+              for (int n = 0; n < NA; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) parts[wave - to][i++][lane] = acc[q][n][j];
+            }
+          }
+          __syncthreads();
+          if (wave < to) {
+            int i = 0;
+#pragma unroll
+            for (int q = 0; q < RT; ++q) {
+              const float mo = parts[wave][i++][lane], lo = parts[wave][i++][lane];
+              const float mx = fmaxf(m[q], mo), mu = mx == -__builtin_inff() ? 0.f : mx;
+              const float mine = exp2_hw(m[q] - mu), other = exp2_hw(mo - mu);
+              m[q] = mx;
+              l[q] = l[q] * mine + lo * other;
+#pragma unroll
+              for (int n = 0; n < NA; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[q][n][j] = acc[q][n][j] * mine + parts[wave][i++][lane] * other;
+            }
+          }
+          __syncthreads();
+        }
+        if (wave != 0) return;
+      }
+    }
+
     // ---- results: the lane's query rows, VW neighbouring dimensions at a time
     asm volatile("" : "+v"(own));
     const int xo = own & 15, go = own >> 4;
@@ -802,12 +939,23 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND>::OCC)) attn_dec
   }
 }
 
-template <typename IO, typename KE, bool BS = false>
+template <typename IO, typename KE, bool BLOCKS = false>
 hipError_t launch_attn_t(const AttnParams& p, int d, dim3 grid, hipStream_t stream) {
-  const bool uni = p.page_size % 16 == 0;
+  // block sizes that kBlocksWide and kBlocksOne do not cover take the general kernel
+  const bool wide = p.block == 4 || p.block == 8 || p.block % 16 == 0;
+  const bool uni = p.page_size % 16 == 0 && (!BLOCKS || wide || p.block == 1);
   const int kind = attn_kind(p.T, p.R);
-#define GDN_ATTN_LAUNCH(DD, UNI, KIND) \
-  hipLaunchKernelGGL((attn_decode_kernel<IO, KE, DD, UNI, KIND, BS>), grid, dim3(256), 0, stream, p)
+#define GDN_ATTN_LAUNCH(DD, UNI, KIND)                                                                              \
+  do {                                                                                                              \
+    if constexpr (!BLOCKS)                                                                                          \
+      hipLaunchKernelGGL((attn_decode_kernel<IO, KE, DD, UNI, KIND, kBlocksNone>), grid, dim3(256), 0, stream, p);   \
+    else if constexpr (!UNI)                                                                                        \
+      hipLaunchKernelGGL((attn_decode_kernel<IO, KE, DD, UNI, KIND, kBlocksAny>), grid, dim3(256), 0, stream, p);    \
+    else if (wide)                                                                                                  \
+      hipLaunchKernelGGL((attn_decode_kernel<IO, KE, DD, UNI, KIND, kBlocksWide>), grid, dim3(256), 0, stream, p);   \
+    else                                                                                                            \
+      hipLaunchKernelGGL((attn_decode_kernel<IO, KE, DD, UNI, KIND, kBlocksOne>), grid, dim3(256), 0, stream, p); \
+  } while (0)
 #define GDN_ATTN_KINDS(DD, UNI)                     \
   if (kind == 0) GDN_ATTN_LAUNCH(DD, UNI, 0);       \
   else if (kind == 1) GDN_ATTN_LAUNCH(DD, UNI, 1);  \
