@@ -353,37 +353,41 @@ def _poison(state, table, lens, page):
     return [kc, vc, ks, vs]
 
 
-@pytest.mark.parametrize("page,block", [(16, 16), (64, 4), (1, 1), (5, 5), (24, 8), (32, 1)])
+# blocks of a multiple of 16, of 8, 4 and 1 token in pages of a multiple of 16; others
+@pytest.mark.parametrize("page,block", [(16, 16), (64, 4), (1, 1), (5, 5), (24, 8), (32, 1), (16, 8), (48, 48), (48, 3), (32, 2)])
+@pytest.mark.parametrize("room", [0, 600])  # tokens that the table has room for beyond: teams of waves, or shares
 @pytest.mark.parametrize("d", [32, 64, 128, 256])
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 @pytest.mark.parametrize("cache", ["e4m3", "int8"])
-def test_types_head_sizes_pages_and_blocks(cache, io, d, page, block):
+def test_types_head_sizes_pages_and_blocks(cache, io, d, room, page, block):
     lens = torch.tensor(LENS, dtype=torch.int32)
-    table, n_pages = paged(LENS, page, seed=d + page)
+    table, n_pages = paged(LENS, page, seed=d + page, width=-(-(max(LENS) + room) // page))
     state = _poison(blocks_cache(n_pages, page, 2, d, block, cache, d * 7 + page), table, lens, page)
     q = torch.randn(len(LENS), 1, 6, d, generator=torch.Generator().manual_seed(d)).to(DT[io])
     _attend(q, state, table, lens, io)
 
 
-@pytest.mark.parametrize("page,block", [(16, 2), (6, 3)])
+@pytest.mark.parametrize("page,block", [(16, 16), (16, 1), (6, 3)])
+@pytest.mark.parametrize("room", [0, 600])
 @pytest.mark.parametrize("T,group", [(1, 16), (1, 20), (2, 3), (4, 8), (64, 1), (16, 6)])
 @pytest.mark.parametrize("io,cache,d", [("bf16", "e4m3", 128), ("bf16", "int8", 256), ("f32", "int8", 64), ("f32", "e4m3", 256),
-                                        ("bf16", "int8", 32)])
-def test_new_tokens_and_groups(io, cache, d, T, group, page, block):
+                                        ("bf16", "int8", 32), ("f32", "int8", 128), ("bf16", "e4m3", 64)])
+def test_new_tokens_and_groups(io, cache, d, T, group, room, page, block):
     lens = torch.tensor([0, 1, T - 1, T, 40, 100, 3 * T + 50], dtype=torch.int32)
-    table, n_pages = paged(lens, page, seed=T)
+    table, n_pages = paged(lens, page, seed=T, width=-(-(int(lens.max()) + room) // page))
     state = _poison(blocks_cache(n_pages, page, 2, d, block, cache, T * 100 + group), table, lens, page)
     q = torch.randn(7, T, 2 * group, d, generator=torch.Generator().manual_seed(T)).to(DT[io])
     _attend(q, state, table, lens, io)
 
 
+@pytest.mark.parametrize("room", [0, 600])
 @pytest.mark.parametrize("io,cache,page,block", [(io, cache, page, block) for io in ("bf16", "f32") for cache in ("e4m3", "int8")
                                                  for page, block in ((32, 1), (6, 1), (16, 16)) if cache == "e4m3" or block == 1])
-def test_values_that_a_token_does_not_see(io, cache, page, block):
+def test_values_that_a_token_does_not_see(io, cache, page, block, room):
     """The newest of several tokens has scales of NaN (its own block's, or where blocks are
     longer, e4m3 codes of NaN; int8 has none): the tokens before it do not see them."""
     lens = torch.tensor([5, 37, 130], dtype=torch.int32)
-    table, n_pages = paged(lens, page)
+    table, n_pages = paged(lens, page, width=-(-(130 + room) // page))
     state = blocks_cache(n_pages, page, 2, 64, block, cache, 11)
     q = torch.randn(3, 4, 4, 64, generator=torch.Generator().manual_seed(3)).to(DT[io])
     refs = [(y, attn_blocks_ref(y, *state, table, lens, 0.125)) for y in (q, q.repeat_interleave(10, 2))]
@@ -421,6 +425,28 @@ def test_split_rows(cache, page, block):
     assert torch.equal(out, again)
     dev = [t.cuda() for t in (q, state[0], state[1], table, lens, state[2], state[3])]
     assert gdn.attn_decode_workspace_size(*dev[:5], k_scale=dev[5], v_scale=dev[6]) > 0
+
+
+@pytest.mark.parametrize("cache", ["e4m3", "int8"])
+@pytest.mark.parametrize("page,block", [(16, 16), (32, 1), (7, 7)])
+@pytest.mark.parametrize("lens", [[512, 500, 1, 0, 300], [65, 128, 3, 96, 127], [64, 33, 7, 0, 2], [512] * 70])
+def test_short_tables(lens, page, block, cache):
+    """Teams at their longest and shortest, one wave alone, and as many rows as teams take (140 heads); entries
+    outside the cache at a wave's first and last tile."""
+    hkv = 2 if len(lens) < 50 else 14
+    table, n_pages = paged(lens, page, spare=0, width=-(-max(lens) // page))
+    table[0, 0], table[0, table.shape[1] // 4], table[1, -1] = -1, n_pages, 1 << 30
+    state = blocks_cache(n_pages, page, hkv, 64, block, cache, 3)
+    q = torch.randn(len(lens), 2, 2 * hkv, 64, generator=torch.Generator().manual_seed(4)).bfloat16()
+    lens = torch.tensor(lens, dtype=torch.int32)
+    some = list(range(len(lens)))[:5]
+    out = gdn.attn_decode(q.cuda(), *(t.cuda() for t in state[:2]), table.cuda(), lens.cuda(), k_scale=state[2].cuda(),
+                          v_scale=state[3].cuda())
+    few = _attend(q[some], state, table[some], lens[some], "bf16")
+    bound = 2 * 2.0 ** -8 * out[some].abs().double() + 1e-4  # the same sums in another order, rounded to bf16
+    assert ((out[some].double() - few.double()).abs() <= bound).all()
+    assert torch.equal(out, gdn.attn_decode(q.cuda(), *(t.cuda() for t in state[:2]), table.cuda(), lens.cuda(),
+                                            k_scale=state[2].cuda(), v_scale=state[3].cuda()))
 
 
 def test_scales_of_a_block_size_that_is_its_page_agree_with_factors_a_head():
