@@ -2,6 +2,7 @@
 (no GPU needed), and the frequencies of long contexts."""
 import ctypes
 import math
+import os
 
 import pytest
 import torch
@@ -255,3 +256,12 @@ def test_frequencies():
                 dict(rot=64, scale=0), dict(rot=64, scaling="parts", trained=10, slow=2, fast=2)):
         with pytest.raises(ValueError):
             gdn.rope_frequencies(**bad)
+
+
+def test_the_short_way_has_no_thread_locals():
+    """One in a library that is loaded late slows every other library's thread-locals down."""
+    import subprocess
+    path = os.path.join(os.path.dirname(L.__file__), "_calls.so")
+    out = subprocess.run(["readelf", "-lW", path], check=True, capture_output=True, text=True).stdout
+    assert " TLS " not in out and "LOAD" in out
+    assert L.calls().rope
