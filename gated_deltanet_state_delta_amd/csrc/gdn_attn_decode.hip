@@ -120,7 +120,12 @@ static int attn_shares(const gdn_attn_decode_args& a) {
   const int alone = tile < 32 ? 64 : 128;
   if (cap <= alone || a.batch > kMostRows || (int64_t)a.batch * a.hq * a.T > (1 << 24)) return 0;
   const int64_t each = (int64_t)a.hkv * attn_tiles(a);  // waves of a share
-  const int64_t fill = 1024 * attn_waves(es, a.d, attn_kind(a.T, a.T * (a.hq / a.hkv))) / each;
+  // Block-scaled caches, bf16 queries, heads of 128 and more, factors at a lane's own place: one wave a SIMD, though
+  // there is room for two (4 rows of 131 072 tokens, 4 heads of 128, e4m3: 90 us, two 99; 256 ragged rows up to 4096, 2
+  // heads of 256, e4m3 104 and 114, int8 106 and 114; heads of 128 in tokens-first pages 1% either way; fp32 queries
+  // 121 and 111, heads of 64 144 and 137).
+  const bool one = a.scale_block > 0 && a.io_dtype == GDN_BF16 && a.d >= 128 && attn_lane_blocks(a.page_size, a.scale_block);
+  const int64_t fill = 1024 * (one ? 1 : attn_waves(es, a.d, attn_kind(a.T, a.T * (a.hq / a.hkv)))) / each;
   const int64_t n = fill < steps ? fill : steps;
   return n < 2 ? 0 : (int)n;
 }

@@ -50,6 +50,10 @@ namespace gdn {
 //  * kBlocksOne: blocks of one token: four factors, likewise;
 //  * kBlocksAny: other sizes: read a tile ahead, a key by each lane, and passed
 //    through LDS.
+// Whether it is one of the first two.
+static inline bool attn_lane_blocks(int page_size, int block) {
+  return page_size % 16 == 0 && (block == 1 || block == 4 || block == 8 || block % 16 == 0);
+}
 constexpr int kBlocksNone = 0, kBlocksWide = 1, kBlocksOne = 2, kBlocksAny = 3;
 
 struct AttnParams {
@@ -212,14 +216,10 @@ __device__ __forceinline__ uint32_t bf_pair(const Raw<N>& r, int i) {
   } else return __builtin_bit_cast(uint32_t, (i & 1) ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r.w[i >> 1], 1.0f, true)
                                                    : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r.w[i >> 1], 1.0f, false));
 }
-// A value at a uniform address that nothing writes during the kernel, through the scalar cache.
-template <typename T> __device__ __forceinline__ T load_const(const T* p) {
-  return *(const __attribute__((address_space(4))) T*)(uintptr_t)p;
-}
-// A pointer that is the same in all lanes, in scalar registers.
+// A pointer into device memory that is the same in all lanes, in scalar registers.
 template <typename T> __device__ __forceinline__ const T* uniform_ptr(const T* p) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)(uint64_t)p), hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)p >> 32));
-  return (const T*)((uint64_t)hi << 32 | lo);
+  return (const T*)(const __attribute__((address_space(1))) T*)((uint64_t)hi << 32 | lo);
 }
 // Elements 2i and 2i+1 of an fp32 piece.
 template <int N>
@@ -424,8 +424,7 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND, BS != kBlocksNo
       Ents o;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const int at = page_of(min(key0 + 16 * n, len - 1));
-        o.e[n] = BS != kBlocksNone ? load_const(tab + at) : tab[at];
+        o.e[n] = tab[page_of(min(key0 + 16 * n, len - 1))];
       }
       return o;
     };
@@ -444,36 +443,56 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND, BS != kBlocksNo
     const int fac_at = BS == kBlocksOne ? 4 * g : p.block >= 16 ? 0 : p.block == 8 ? g >> 1 : g;
     const float* kfac = p.k_blocks + (int64_t)h * p.nblk;
     const float* vfac = p.v_blocks + (int64_t)h * p.nblk;
-    // LANE: what K's and V's loads of a subtile share, found a tile ahead for K.
-    struct Sub { int ent, off, blk, rows; bool ok; };  // entry (0 where there is none), first slot, its block, rows that exist
+    // LANE: where the next 64 subtiles lie, one to a lane: byte offsets of their
+    // rows in K and V, the place of their first factor, and whether they are held.
+    // A tile reads its subtiles' from the lanes: a third of the instructions that
+    // finding each by itself in scalar registers took.
+    struct { int64_t k, v, f; } spot = {};
+    uint64_t spot_ok = 0;
+    int spot_ent = 0;  // the table entries of the 64 behind
+    auto spot_load = [&](int key) { return tab[page_of(min(key + 16 * lane, len - 1))]; };
+    auto spot_fill = [&](int first) {
+      const int key = first + 16 * lane, off = key - page_of(key) * p.page_size;
+      const bool ok = key < c1 && spot_ent >= 0 && spot_ent < p.n_pages;
+      const int64_t e = ok ? spot_ent : 0;
+      spot.k = e * p.k_sp + (int64_t)off * p.k_st;
+      spot.v = e * p.v_sp + (int64_t)off * p.v_st;
+      spot.f = e * p.blk_sp + (int)(((uint64_t)(uint32_t)off * p.blk_mul) >> p.blk_shift);
+      spot_ok = __ballot(ok);
+      spot_ent = spot_load(first + 1024);
+    };
+    auto from_lane = [&](int64_t v, int l) {
+      const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)v, l), hi = __builtin_amdgcn_readlane((uint32_t)((uint64_t)v >> 32), l);
+      return (int64_t)((uint64_t)hi << 32 | lo);
+    };
+    struct Sub { int64_t k, v, f; int rows; bool ok; };
     struct Subs { Sub s[LANE ? NT : 1]; } sub_cur = {}, sub_next = {};
-    auto find_subs = [&](const Ents& en, int key0) {
+    auto find_subs = [&](int key0) {
+      const int at = (key0 - c0) >> 4 & 63;
+      if (at == 0) spot_fill(key0);
       Subs o = {};
 #pragma unroll
       for (int n = 0; n < (LANE ? NT : 0); ++n) {
         Sub& s = o.s[n];
-        const int key = key0 + 16 * n;
-        s.ok = en.e[n] >= 0 && en.e[n] < p.n_pages;
-        s.ent = s.ok ? en.e[n] : 0;
-        s.off = key - page_of(key) * p.page_size;
-        s.blk = (int)(((uint64_t)(uint32_t)s.off * p.blk_mul) >> p.blk_shift);
-        s.rows = s.ok && key < c1 ? min(16, len - key) : 0;
+        s.ok = (spot_ok >> (at + n)) & 1;
+        s.k = from_lane(spot.k, at + n);
+        s.v = from_lane(spot.v, at + n);
+        s.f = from_lane(spot.f, at + n);
+        s.rows = s.ok ? min(16, len - key0 - 16 * n) : 0;
       }
       return o;
     };
-    auto rows_of = [&](const char* base, int64_t sp, uint32_t st, const Sub& s) {
-      return buf_rsrc_n(base + s.ent * sp + (int64_t)s.off * st, s.rows > 0 ? (uint32_t)(s.rows - 1) * st + D * ES : 0u);
+    auto rows_at = [&](const char* base, int64_t at, uint32_t st, int rows) {
+      return buf_rsrc_n(base + at, rows > 0 ? (uint32_t)(rows - 1) * st + D * ES : 0u);
     };
-    auto load_factors = [&](const float* base, const Sub& s) {
-      return *reinterpret_cast<const Four*>(base + s.ent * p.blk_sp + s.blk + fac_at);
-    };
+    auto load_factors = [&](const float* base, int64_t at) { return *reinterpret_cast<const Four*>(base + at + fac_at); };
     auto factor_of = [&](const Four& f, int j) { return f[BS == kBlocksOne ? j : 0]; };
     Four kf[LANE ? NT : 1], vf[LANE ? NT : 1];
     auto issue_k_uni = [&](const Ents& en, const Subs& su, int key0) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        if constexpr (LANE) kf[n] = load_factors(kfac, su.s[n]);
-        const auto rs = LANE ? rows_of(kbase, p.k_sp, p.k_st, su.s[LANE ? n : 0]) : sub_rsrc(kbase, p.k_sp, p.k_st, en.e[n], key0 + 16 * n);
+        if constexpr (LANE) kf[n] = load_factors(kfac, su.s[n].f);
+        const auto rs = LANE ? rows_at(kbase, su.s[LANE ? n : 0].k, p.k_st, su.s[LANE ? n : 0].rows) : sub_rsrc(kbase, p.k_sp, p.k_st, en.e[n], key0 + 16 * n);
 #pragma unroll
         for (int c = 0; c < NC; ++c) kr[n][c] = raw_buf<KW * ES, ONCE>(rs, x * p.k_st + (4 * KW * c + KW * g) * ES);
       }
@@ -481,8 +500,8 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND, BS != kBlocksNo
     auto issue_v_uni = [&](const Ents& en, const Subs& su, int key0) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        if constexpr (LANE) vf[n] = load_factors(vfac, su.s[n]);
-        const auto rs = LANE ? rows_of(vbase, p.v_sp, p.v_st, su.s[LANE ? n : 0]) : sub_rsrc(vbase, p.v_sp, p.v_st, en.e[n], key0 + 16 * n);
+        if constexpr (LANE) vf[n] = load_factors(vfac, su.s[n].f);
+        const auto rs = LANE ? rows_at(vbase, su.s[LANE ? n : 0].v, p.v_st, su.s[LANE ? n : 0].rows) : sub_rsrc(vbase, p.v_sp, p.v_st, en.e[n], key0 + 16 * n);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -546,10 +565,14 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND, BS != kBlocksNo
     int par = 0;
     if (c0 < c1) {
       if constexpr (UNI) {
-        ent_cur = load_ents(c0);
-        sub_cur = find_subs(ent_cur, c0);
+        if constexpr (LANE) {
+          spot_ent = spot_load(c0);
+          sub_cur = find_subs(c0);
+        } else {
+          ent_cur = load_ents(c0);
+        }
         issue_k_uni(ent_cur, sub_cur, c0);
-        ent_next = load_ents(c0 + KT);
+        if constexpr (!LANE) ent_next = load_ents(c0 + KT);
       } else {
         const int ent1 = load_ent1(c0);
         publish(ent1, c0, 0);
@@ -627,12 +650,15 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND, BS != kBlocksNo
 #pragma unroll
         for (int n = 0; n < NT; ++n)
           if (LANE ? !sub_cur.s[LANE ? n : 0].ok : ent_cur.e[n] < 0 || ent_cur.e[n] >= p.n_pages) sub_ok &= ~(1u << n);
-        if constexpr (LANE) sub_next = find_subs(ent_next, key0 + KT);
+        if constexpr (LANE) sub_next = find_subs(key0 + KT);
         // LANE: always, with no rows past the end, so that the values' wait need not count these loads in
         if (LANE || key0 + KT < c1) issue_k_uni(ent_next, sub_next, key0 + KT);
-        sub_cur = sub_next;
-        ent_cur = ent_next;
-        ent_next = load_ents(key0 + 2 * KT);
+        if constexpr (LANE) {
+          sub_cur = sub_next;
+        } else {
+          ent_cur = ent_next;
+          ent_next = load_ents(key0 + 2 * KT);
+        }
       } else {
         par ^= 1;
         if (BS != kBlocksNone || key0 + KT < c1) {
@@ -941,9 +967,8 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND, BS != kBlocksNo
 
 template <typename IO, typename KE, bool BLOCKS = false>
 hipError_t launch_attn_t(const AttnParams& p, int d, dim3 grid, hipStream_t stream) {
-  // block sizes that kBlocksWide and kBlocksOne do not cover take the general kernel
-  const bool wide = p.block == 4 || p.block == 8 || p.block % 16 == 0;
-  const bool uni = p.page_size % 16 == 0 && (!BLOCKS || wide || p.block == 1);
+  const bool wide = p.block != 1;
+  const bool uni = BLOCKS ? attn_lane_blocks(p.page_size, p.block) : p.page_size % 16 == 0;
   const int kind = attn_kind(p.T, p.R);
 #define GDN_ATTN_LAUNCH(DD, UNI, KIND)                                                                              \
   do {                                                                                                              \
