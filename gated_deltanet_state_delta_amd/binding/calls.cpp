@@ -267,7 +267,7 @@ PyObject* kv_read(PyObject*, PyObject* const* v, Py_ssize_t n) {
       !cache_fields(a, kc, in.tensor(1), in.tensor(2), lens, ks, vs, rows, hkv, d, k, w))
     Py_RETURN_NONE;
   a.total_tokens = cu ? tokens : rows * tokens;
-  if (a.total_tokens > (int64_t(1) << 28)) Py_RETURN_NONE;  // before memory is taken for it
+  if (a.total_tokens > (int64_t(1) << 28) || rows == 0) Py_RETURN_NONE;  // before memory is taken for it; not launched
   const auto options = kc->options().dtype(a.io_dtype == GDN_BF16 ? at::kBFloat16 : at::kFloat);
   Tensor out[2];
   for (Tensor& t : out) t = cu ? at::empty({tokens, hkv, d}, options) : at::empty({rows, tokens, hkv, d}, options);
@@ -317,7 +317,7 @@ PyObject* rope(PyObject*, PyObject* const* v, Py_ssize_t n) {
     a.positions_i64 = pos->scalar_type() == at::kLong;
   } else {
     const int64_t rows = lens->dim() == 1 ? lens->size(0) : -1;
-    if (rows < 0 || !fits(rows) || !ints(*lens, rows) || (cu ? dim != 3 || !ints(*cu, rows + 1) : dim != 4 || lead[0] != rows))
+    if (rows < 1 || !fits(rows) || !ints(*lens, rows) || (cu ? dim != 3 || !ints(*cu, rows + 1) : dim != 4 || lead[0] != rows))
       Py_RETURN_NONE;
     a.batch = static_cast<int32_t>(rows);
     a.lens = static_cast<const int32_t*>(lens->data_ptr());

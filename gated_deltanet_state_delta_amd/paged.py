@@ -366,7 +366,7 @@ def kv_read_args(k_cache, v_cache, page_table, lens, tokens, *, cu_seqlens=None,
         raise ValueError("tokens must be a whole number of at least 0, got %s" % (tokens,))
     tokens = int(tokens)
     if dtype is None:
-        dtype = out[0].dtype if out is not None else k_cache.dtype if k_cache.dtype in _IO else torch.bfloat16
+        dtype = out[0].dtype if out else k_cache.dtype if k_cache.dtype in _IO else torch.bfloat16
     if dtype not in _IO:
         raise ValueError("unsupported dtype %s (float32 or bfloat16)" % dtype)
     cache_dtype, factors, blocks, kcs, vcs = _caches(dtype, k_cache, v_cache, cs, k_scale, v_scale, hkv, d)
@@ -377,11 +377,14 @@ def kv_read_args(k_cache, v_cache, page_table, lens, tokens, *, cu_seqlens=None,
         cu_seqlens = _i32(cu_seqlens, "cu_seqlens", (B + 1,))
     new = out is None
     if new:
-        out = tuple(torch.empty(shape, dtype=dtype, device=k_cache.device) for _ in range(2))
+        make = torch.empty if B else torch.zeros  # (a batch of no rows is not launched)
+        out = tuple(make(shape, dtype=dtype, device=k_cache.device) for _ in range(2))
     else:
-        for t in out:
-            if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or t.data_ptr() % 16:
-                raise ValueError("out must be two contiguous, 16-byte aligned %s %s" % (dtype, tuple(shape)))
+        if len(out) != 2 or any(t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or t.data_ptr() % 16
+                                for t in out):
+            raise ValueError("out must be two contiguous, 16-byte aligned %s %s" % (dtype, tuple(shape)))
+        if out[0].numel() and out[0].data_ptr() == out[1].data_ptr():
+            raise ValueError("out's two tensors must be apart")
     table, table_stride, max_pages = _table(page_table, B)
     lens = _i32(lens, "lens", (B,))
     a = _lib.KvReadArgs(

@@ -108,6 +108,10 @@ def rope_args(q, k, inv_freq, *, lens=None, cu_seqlens=None, positions=None, int
         elif len(shape) != 4 or shape[0] != batch:
             raise ValueError("without cu_seqlens q and k must be [B, T, heads, d]")
         lens = _i32(lens, "lens", (batch,))
+    if out is not None and len(out) != 2:
+        raise ValueError("out must be (q, k)")
+    # tokens of no row: zeros where all of it is new
+    make = torch.zeros if (cu_seqlens is not None and out is not None) or (lens is not None and batch == 0) else torch.empty
     ins, outs = [], []
     for n, x in enumerate((q, k)):
         if x is None:
@@ -117,7 +121,7 @@ def rope_args(q, k, inv_freq, *, lens=None, cu_seqlens=None, positions=None, int
         ins.append(_strides(x))
         y = None if out is None else out[n]
         if y is None:
-            y = torch.empty(x.shape, dtype=dtype, device=x.device)
+            y = make(x.shape, dtype=dtype, device=x.device)
         elif y.shape != x.shape or y.dtype is not dtype:
             raise ValueError("out must have the inputs' shapes and dtype")
         to = _strides(y)

@@ -540,8 +540,8 @@ gdn_status gdn_attn_decode(const gdn_attn_decode_args* args, void* stream);
  *         batch tokens each (a whole number).  Where offsets decrease, tokens
  *         may be left out; none goes anywhere but to its place in a row whose
  *         range holds it
- * Rows whose new tokens fall into one page slot race (rows share full pages
- * only: see gdn_pages_fork).  total_tokens is at most 2^28.  batch == 0 or
+ * Rows whose new tokens fall into one page slot race, with block scales into one
+ * block (rows share full pages only: see gdn_pages_fork).  total_tokens is at most 2^28.  batch == 0 or
  * total_tokens == 0 is a no-op.
  * ------------------------------------------------------------------------- */
 typedef struct {

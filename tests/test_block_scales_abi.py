@@ -168,7 +168,8 @@ def test_binding_passes_block_scales():
     dict(tokens=-1), dict(tokens=1.5), dict(dtype=torch.float16), dict(lens=torch.zeros(2, 1)), dict(lens=torch.zeros(2)),
     dict(cu_seqlens=torch.zeros(2, dtype=torch.int32)), dict(k_cache=I8[0]), dict(page_table=torch.zeros(3, 4, dtype=torch.int32)),
     dict(out=(torch.zeros(2, 3, 2, 64), torch.zeros(2, 3, 2, 32))), dict(out=(torch.zeros(2, 2, 3, 64).transpose(1, 2),) * 2),
-    dict(out=(torch.zeros(2, 3, 2, 64), torch.zeros(2, 3, 2, 64).bfloat16())),
+    dict(out=(torch.zeros(2, 3, 2, 64), torch.zeros(2, 3, 2, 64).bfloat16())), dict(out=(torch.zeros(2, 3, 2, 64),)),
+    dict(out=(torch.zeros(2, 3, 2, 64),) * 2), dict(out=()),
 ])
 def test_kv_read_args_refuse(over):
     kw = dict(k_cache=I8, v_cache=I8, page_table=torch.zeros(2, 4, dtype=torch.int32), lens=torch.zeros(2, dtype=torch.int32),
@@ -189,6 +190,18 @@ def test_kv_read_args_shapes():
     assert out[0] is given[0] and not a.zero_rest
 
 
+def test_batches_of_no_rows_read_and_turn_to_zeros():
+    none, cu = torch.zeros(0, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    _, _, out = gdn.kv_read_args(I8, I8, torch.zeros(0, 4, dtype=torch.int32), none, 5, cu_seqlens=cu, k_scale=S, v_scale=S)
+    assert all(t.shape == (5, 2, 64) and (t == 0).all() for t in out)
+    _, _, out = gdn.rope_args(torch.ones(5, 2, 64), None, F, lens=none, cu_seqlens=cu)
+    assert (out[0] == 0).all()
+    # one output given, one new: the new one's tokens of no row are zeros
+    q, k = torch.ones(5, 2, 64), torch.ones(5, 1, 64)
+    a, _, out = gdn.rope_args(q, k, F, lens=none[:0].new_zeros(1), cu_seqlens=torch.tensor([0, 2]), out=(q, None))
+    assert out[0] is q and (out[1] == 0).all() and not a.zero_rest
+
+
 Q, K, F = torch.zeros(2, 3, 4, 64), torch.zeros(2, 3, 2, 64), torch.ones(16, dtype=torch.float64)
 LENS = torch.zeros(2, dtype=torch.int32)
 
@@ -201,7 +214,7 @@ LENS = torch.zeros(2, dtype=torch.int32)
     dict(cu_seqlens=torch.zeros(3, dtype=torch.int32)), dict(q=Q[0], k=K[0]),
     dict(lens=None, positions=torch.zeros(2, 3, dtype=torch.int64), cu_seqlens=torch.zeros(3, dtype=torch.int32)),
     dict(out=(Q[:1], K)), dict(out=(Q.bfloat16(), K)), dict(out=(torch.zeros(1, 3, 4, 64).expand(2, 3, 4, 64), K)),
-    dict(out=(torch.zeros(2, 3, 64, 4).transpose(2, 3), K)),
+    dict(out=(torch.zeros(2, 3, 64, 4).transpose(2, 3), K)), dict(out=(Q,)), dict(out=()),
 ])
 def test_rope_args_refuse(over):
     with pytest.raises(ValueError):

@@ -462,6 +462,51 @@ def test_scales_of_a_block_size_that_is_its_page_agree_with_factors_a_head():
     assert torch.allclose(a, b, rtol=1e-4, atol=1e-6)
 
 
+def test_thousands_of_rows():
+    """More rows than are dealt into shares, with tables longer than teams take."""
+    rows, g = 5000, torch.Generator().manual_seed(1)
+    lens = torch.randint(0, 40, (rows,), generator=g).to(torch.int32)
+    lens[17] = 530
+    need = (lens + 15) // 16
+    n_pages, table, at = int(need.sum()), torch.full((rows, 40), -1, dtype=torch.int32), 0
+    for b, n in enumerate(need.tolist()):
+        table[b, :n], at = torch.arange(at, at + n), at + n
+    state = blocks_cache(n_pages, 16, 1, 32, 16, "int8", 1)
+    q = torch.randn(rows, 1, 2, 32, generator=g).bfloat16()
+    out = gdn.attn_decode(q.cuda(), state[0].cuda(), state[1].cuda(), table.cuda(), lens.cuda(), k_scale=state[2].cuda(),
+                          v_scale=state[3].cuda()).double().cpu()
+    some = [0, 17, 18, 999, 4097, 4999] + torch.randint(0, rows, (40,), generator=g).tolist()
+    want, _, mean, size = attn_blocks_ref(q[some], *state, table[some], lens[some], 32 ** -0.5)
+    assert ((out[some] - want).abs() <= attn_blocks_bound(want, mean, size, lens[some], 32, "bf16")).all()
+    # and one token appended to each
+    lens = lens + 1
+    fresh = (lens - 1) % 16 == 0
+    extra = torch.arange(n_pages, n_pages + int(fresh.sum()), dtype=torch.int32)
+    table[fresh, ((lens - 1) // 16)[fresh].long()] = extra
+    state = blocks_cache(n_pages + len(extra), 16, 1, 32, 16, "int8", 2)
+    x = torch.randn(rows, 1, 1, 32, generator=g).bfloat16()
+    dev = [t.cuda() for t in state]
+    gdn.kv_append(x.cuda(), x.cuda(), dev[0], dev[1], table.cuda(), lens.cuda(), k_scale=dev[2], v_scale=dev[3])
+    want = append_ref(state[0], state[2], x[:, 0], [1] * rows, table, lens, "int8")
+    assert torch.equal(dev[0].cpu(), want[0]) and torch.equal(dev[2].cpu(), want[1])
+
+
+def test_no_pages_no_rows_no_tokens():
+    """Caches of no pages, tables of no entries, batches of no rows, rows of no tokens."""
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32).cuda()
+    for n_pages, width, rows in ((0, 4, 3), (2, 0, 3), (2, 4, 0), (0, 0, 3)):
+        c = [torch.zeros(n_pages, 16, 2, 64, dtype=torch.int8).cuda() for _ in range(2)]
+        s = [torch.ones(n_pages, 2, 4).cuda() for _ in range(2)]
+        kw, table, lens = dict(k_scale=s[0], v_scale=s[1]), i32(rows, width), i32(rows) + 20
+        q = torch.ones(rows, 1, 4, 64).bfloat16().cuda()
+        out = gdn.attn_decode(q, *c, table, lens, **kw)
+        assert out.shape == q.shape and (out == 0).all()
+        gdn.kv_append(q[:, :, :2], q[:, :, :2], *c, table, lens, **kw)
+        for got in (gdn.kv_read(*c, table, lens, 3, **kw), gdn.kv_read(*c, table, lens, 7, cu_seqlens=i32(rows + 1), **kw)):
+            assert all((t == 0).all() for t in got)
+        assert all((t == 0).all() for t in gdn.kv_read(*c, table, lens, 0, **kw))
+
+
 # ----------------------------------------------------------- all of it at once --
 
 
