@@ -308,7 +308,14 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND, BS != kBlocksNo
   // Where no second wave reads a key, non-temporal loads leave the caches
   // alone (the bf16 batch above, at two waves of 8 KiB: 184 us against 201 with
   // ordinary ones; 64 rows that share all of their 4096 tokens 94 against 85).
-  constexpr bool BF = C::BF, MT = KIND > 0, ONCE = KIND < 2 || (KIND == 2 && RT == 2);
+  // Block-scaled rows of less than 128 bytes lie in one line with the next head's,
+  // which stays in the caches for the wave that takes that head (64 ragged rows of
+  // up to 8192 tokens, 16 heads of 64, e4m3: 126 us against 136; of 32: 101 against
+  // 129).  In caches of heads first there is no such neighbour and this costs 11%
+  // (108 us against 97); a branch on the strides here costs every layout its
+  // overlapped loads (133 us).
+  constexpr bool BF = C::BF, MT = KIND > 0;
+  constexpr bool ONCE = (KIND < 2 || (KIND == 2 && RT == 2)) && (BS == kBlocksNone || D * ES >= 128);
   constexpr uint64_t kNone = ~0ull;
   __shared__ uint64_t offs[UNI ? 1 : 4][2][2][UNI ? 1 : KT];  // [wave][parity][K, V][key]
   __shared__ __align__(16) float blocks[BS == kBlocksAny ? 4 : 1][2][BS == kBlocksAny ? KT : 4];  // [wave][K, V][key]: a tile's scales
