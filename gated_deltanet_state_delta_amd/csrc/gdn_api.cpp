@@ -534,6 +534,8 @@ gdn_status gdn_rope(const gdn_rope_args* p, void* stream) {
     return fail(GDN_ERR_NULL, "%s: q, q_out, inv_freq and positions or lens are required", f);
   if ((a.hkv > 0) != (a.k != nullptr) || (a.k != nullptr) != (a.k_out != nullptr))
     return fail(GDN_ERR_NULL, "%s: k, k_out and hkv go together", f);
+  if (a.k && (a.q_out == a.k || a.k_out == a.q || a.q_out == a.k_out))
+    return fail(GDN_ERR_LAYOUT, "%s: one input's output is the other, or its output", f);
   if (!aligned(a.inv_freq, 8) || (a.positions && !aligned(a.positions, a.positions_i64 ? 8 : 4)))
     return fail(GDN_ERR_LAYOUT, "%s: inv_freq and positions must be aligned to their elements", f);
   gdn_status st = rope_layout(f, "q", a, a.hq, a.q, a.q_stride_token, a.q_stride_head, a.q_out, a.qo_stride_token, a.qo_stride_head);

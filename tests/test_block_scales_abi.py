@@ -106,6 +106,7 @@ def _rope(**over):
     (dict(q_stride_token=-384), 4), (dict(qo_stride_head=-1), 4), (dict(k_stride_token=1 << 40), 4),
     (dict(q_out=FAKE, qo_stride_token=400), 4), (dict(k_out=FAKE * 2, ko_stride_head=32), 4),  # in place, other strides
     (dict(q_out=FAKE + 64), 4), (dict(k_out=FAKE * 2 + 512), 4),                                # partly over the input
+    (dict(q_out=FAKE * 2), 4), (dict(k_out=FAKE), 4), (dict(k_out=FAKE * 3), 4),                # over the other's
 ])
 def test_rope_refuses(over, status):
     assert L.load().gdn_rope(ctypes.byref(_rope(**over)), None) == status, L.load().gdn_last_error()
