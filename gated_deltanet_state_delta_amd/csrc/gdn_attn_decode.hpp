@@ -56,7 +56,7 @@ namespace gdn {
 // twice: the places of 64 subtiles are found at a time, one to a lane, and a tile
 // whose keys every row sees has no masks.  4 rows of 131 072 tokens, 4 heads of 128,
 // e4m3, a block a page, 537 MB: 89 us = 6.0 TB/s, 98 without these; 64 ragged rows
-// up to 8192 tokens, 8 heads of 128, int8, blocks of one token, 572 MB: 107 us = 5.3
+// up to 8192 tokens, 8 heads of 128, int8, blocks of one token, 572 MB: 105 us = 5.4
 // TB/s, where the factors of every key are loaded and multiplied in besides.  Rows
 // of 64 bytes stay at 4.5 TB/s, of 32 at 2.8.
 // Whether it is one of the first two.
@@ -807,13 +807,22 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND, BS != kBlocksNo
 #pragma unroll
             for (int e2 = 0; e2 < VW / 2; ++e2) {
               uint32_t c[4 * NP];
+              if constexpr (!std::is_same<KE, i8>::value) {
 #pragma unroll
-              for (int j = 0; j < 4 * NP; ++j) c[j] = bf_pair<KE>(vr[a + (j >> 2)][j & 3][u], e2);
+                for (int j = 0; j < 4 * NP; ++j) c[j] = bf_pair<KE>(vr[a + (j >> 2)][j & 3][u], e2);
+              }
               // V^T's operand for the pieces' lower or upper elements
               auto dims = [&](const uint32_t* cc, int half, bf4* t) {
 #pragma unroll
                 for (int i = 0; i < NP; ++i) {
                   uint2 w;
+                  if constexpr (std::is_same<KE, i8>::value) {  // two keys' elements, converted, into one register (107 us -> 105)
+                    auto value = [&](int j) { return __float_as_uint((float)(int8_t)(vr[a + i][j][u].w[e2 >> 1] >> (16 * (e2 & 1) + 8 * half))); };
+                    w.x = __builtin_amdgcn_perm(value(1), value(0), 0x07060302u);
+                    w.y = __builtin_amdgcn_perm(value(3), value(2), 0x07060302u);
+                    t[i] = __builtin_bit_cast(bf4, w);
+                    continue;
+                  }
                   w.x = __builtin_amdgcn_perm(cc[4 * i + 1], cc[4 * i], half ? 0x07060302u : 0x05040100u);
                   w.y = __builtin_amdgcn_perm(cc[4 * i + 3], cc[4 * i + 2], half ? 0x07060302u : 0x05040100u);
                   t[i] = __builtin_bit_cast(bf4, w);
@@ -823,7 +832,7 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND, BS != kBlocksNo
                 if constexpr (NP == 2) return mma_k32(in, t[0], t[1], pw[q][k][0], pw[q][k][1]);
                 else return mma_k16(in, t[0], pw[q][k][0]);
               };
-              if (!MT || !apart) {
+              if (!MT || std::is_same<KE, i8>::value || !apart) {
                 bf4 t[2][NP];
                 dims(c, 0, t[0]);
                 dims(c, 1, t[1]);
