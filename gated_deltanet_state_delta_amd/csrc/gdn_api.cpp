@@ -476,6 +476,8 @@ gdn_status gdn_kv_append(const gdn_kv_append_args* p, void* stream) {
   // its blocks are counted in 32 bits, 64 to a workgroup
   if (a.total_tokens / a.scale_block + 2 * (int64_t)a.batch >= (int64_t(1) << 29))
     return fail(GDN_ERR_UNSUPPORTED, "%s: total_tokens / scale_block + 2 * batch must be below 2^29", f);
+  if (a.k_cache == a.v_cache || a.k_block_scale == a.v_block_scale)
+    return fail(GDN_ERR_LAYOUT, "%s: one cache, or its block scales, for keys and values", f);
   return from_hip(gdn::launch_kv_quantise(a, (hipStream_t)stream), "gdn_kv_append launch");
 }
 

@@ -531,7 +531,8 @@ gdn_status gdn_attn_decode(const gdn_attn_decode_args* args, void* stream);
  * token at the block's first slot starts it anew: what its scale and codes held
  * does not matter.  NaN is a code of GDN_E4M3; GDN_I8 has none, so NaN in a
  * token makes its block's scale NaN.  A scale that is NaN stays so.
- * total_tokens / scale_block + 2 * batch is below 2^29.
+ * total_tokens / scale_block + 2 * batch is below 2^29, and K and V have
+ * caches and block scales of their own (one start for both: GDN_ERR_LAYOUT).
  *
  *   k, v  [total_tokens, hkv, d] io_dtype, strides {token, head}
  *   cu_seqlens  [batch + 1] int32, non-decreasing: row b's tokens are

@@ -65,6 +65,13 @@ def test_too_many_blocks_are_refused():
     assert lib.gdn_kv_append(ctypes.byref(a), None) == 5 and b"2 * batch" in lib.gdn_last_error()
 
 
+@pytest.mark.parametrize("over", [dict(), dict(v_cache=FAKE * 2), dict(v_block_scale=FAKE * 2)])
+def test_keys_and_values_have_caches_and_scales_of_their_own(over):
+    lib = L.load()
+    a = _append(**{**BLOCKS, "k_cache": FAKE, "v_cache": FAKE, "k_block_scale": FAKE, "v_block_scale": FAKE, **over})
+    assert lib.gdn_kv_append(ctypes.byref(a), None) == 4 and b"for keys and values" in lib.gdn_last_error()
+
+
 def test_nothing_to_do_needs_no_launch():
     lib = L.load()
     for over in (dict(batch=0), dict(total_tokens=0)):
