@@ -12,7 +12,9 @@ namespace gdn {
 // through LDS) up to 256 rows, four up to 1024, one beyond.  Attention and
 // join with sixteen and with four: 12 rows of hundreds of parts (3 rows of
 // 19 620 tokens, fp32) 32.8 and 34.8 us, 18 rows (19 870 tokens, heads of 256)
-// 42.0 and 45.8, 156 rows of few parts the same.
+// 42.0 and 45.8, 156 rows of few parts the same.  Four also for up to 32 parts a
+// row of a block-scaled cache, which they load at once (1 row of 1003 tokens, 8
+// heads of 128: 9.6 us against 10.1; 4 rows 10.6 and 11.2; 2 rows of 1500 the same).
 template <typename IO, int D, int WPR>
 __global__ void __launch_bounds__(WPR > 1 ? 64 * WPR : 256) attn_join_kernel(AttnParams p) {
   constexpr int V = D < 64 ? 1 : D / 64;  // dimensions of a lane (the first 32 lanes' for D = 32)
@@ -87,7 +89,8 @@ __global__ void __launch_bounds__(WPR > 1 ? 64 * WPR : 256) attn_join_kernel(Att
 template <typename IO, int D>
 static void launch_join_d(const AttnParams& p, hipStream_t stream) {
   const int64_t rows = (int64_t)p.batch * p.hkv * p.R;
-  if (rows <= 256) hipLaunchKernelGGL((attn_join_kernel<IO, D, 16>), dim3((unsigned)rows), dim3(1024), 0, stream, p);
+  const bool few_parts = p.block > 0 && p.shares <= 32 * (int64_t)p.batch;
+  if (rows <= 256 && !few_parts) hipLaunchKernelGGL((attn_join_kernel<IO, D, 16>), dim3((unsigned)rows), dim3(1024), 0, stream, p);
   else if (rows <= 1024) hipLaunchKernelGGL((attn_join_kernel<IO, D, 4>), dim3((unsigned)rows), dim3(256), 0, stream, p);
   else hipLaunchKernelGGL((attn_join_kernel<IO, D, 1>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, p);
 }
