@@ -20,7 +20,7 @@ STATUS_NAMES = {0: "GDN_OK", 1: "GDN_ERR_NULL", 2: "GDN_ERR_SHAPE", 3: "GDN_ERR_
                 4: "GDN_ERR_LAYOUT", 5: "GDN_ERR_UNSUPPORTED", 6: "GDN_ERR_HIP"}
 
 # every extern "C" symbol include/libgdn.h declares
-EXPORTED = ("gdn_last_error", "gdn_version", "gdn_gate", "gdn_prefill", "gdn_prefill_workspace_size",
+EXPORTED = ("gdn_last_error", "gdn_version", "gdn_header_digest", "gdn_gate", "gdn_prefill", "gdn_prefill_workspace_size",
             "gdn_prefill_noalloc", "gdn_decode", "gdn_conv1d", "gdn_wait_timeouts",
             "gdn_attn_decode", "gdn_attn_decode_workspace_size", "gdn_kv_append", "gdn_kv_read", "gdn_rope",
             "gdn_pages_copy",
@@ -157,6 +157,8 @@ def load(path: str | None = None):
         lib.gdn_last_error.argtypes = []
         lib.gdn_version.restype = ctypes.c_char_p
         lib.gdn_version.argtypes = []
+        lib.gdn_header_digest.restype = ctypes.c_char_p
+        lib.gdn_header_digest.argtypes = []
         lib.gdn_gate.restype = ctypes.c_int
         lib.gdn_gate.argtypes = [_vp, _vp, _vp, _vp, _i32, _i64, _i32, _vp, _vp, _vp, _vp]
         lib.gdn_prefill_workspace_size.restype = ctypes.c_size_t
@@ -198,7 +200,8 @@ def load(path: str | None = None):
 
 
 def calls():
-    """The module _calls (binding/calls.cpp), bound to the library."""
+    """The module _calls (binding/calls.cpp), bound to the library.  Binding raises
+    where the two were built from different headers."""
     global _calls
     if _calls is None:
         lib = load()
@@ -206,7 +209,7 @@ def calls():
             raise RuntimeError("_calls.so is not built; run `python -m gated_deltanet_state_delta_amd.build`")
         from . import _calls as module
         module.bind(*(ctypes.cast(getattr(lib, "gdn_" + name), _vp).value for name in
-                      ("attn_decode", "attn_decode_workspace_size", "kv_append", "kv_read", "rope")))
+                      ("header_digest", "attn_decode", "attn_decode_workspace_size", "kv_append", "kv_read", "rope")))
         _calls = module
     return _calls
 

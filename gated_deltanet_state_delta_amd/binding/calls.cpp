@@ -17,6 +17,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 
 #include "../../include/libgdn.h"
 
@@ -356,22 +357,28 @@ PyObject* rope(PyObject*, PyObject* const* v, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// bind(attn_decode, attn_decode_workspace_size, kv_append, kv_read, rope): libgdn's entry points, as addresses.
+// bind(header_digest, attn_decode, attn_decode_workspace_size, kv_append, kv_read, rope): libgdn's entry
+// points, as addresses.  The structs that they take are laid out by the header, so one of another header is refused.
 PyObject* bind(PyObject*, PyObject* const* v, Py_ssize_t n) {
-  if (!count_is(n, 5)) return nullptr;
-  void* p[5];
-  for (int i = 0; i < 5; ++i) {
+  if (!count_is(n, 6)) return nullptr;
+  void* p[6];
+  for (int i = 0; i < 6; ++i) {
     p[i] = PyLong_AsVoidPtr(v[i]);
     if (!p[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "no address");
       return nullptr;
     }
   }
-  g_attn = reinterpret_cast<decltype(g_attn)>(p[0]);
-  g_attn_workspace = reinterpret_cast<decltype(g_attn_workspace)>(p[1]);
-  g_append = reinterpret_cast<decltype(g_append)>(p[2]);
-  g_read = reinterpret_cast<decltype(g_read)>(p[3]);
-  g_rope = reinterpret_cast<decltype(g_rope)>(p[4]);
+  const char* digest = reinterpret_cast<decltype(&gdn_header_digest)>(p[0])();
+  if (!digest || std::strcmp(digest, GDN_HEADER_DIGEST) != 0) {
+    PyErr_SetString(PyExc_RuntimeError, "_calls.so and libgdn.so were built from different headers; build both again");
+    return nullptr;
+  }
+  g_attn = reinterpret_cast<decltype(g_attn)>(p[1]);
+  g_attn_workspace = reinterpret_cast<decltype(g_attn_workspace)>(p[2]);
+  g_append = reinterpret_cast<decltype(g_append)>(p[3]);
+  g_read = reinterpret_cast<decltype(g_read)>(p[4]);
+  g_rope = reinterpret_cast<decltype(g_rope)>(p[5]);
   Py_RETURN_NONE;
 }
 

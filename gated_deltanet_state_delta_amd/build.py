@@ -11,7 +11,9 @@ from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import hashlib
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -56,6 +58,17 @@ def hipcc() -> str:
     return cand if os.path.exists(cand) else (shutil.which("hipcc") or "hipcc")
 
 
+def header_digest() -> str:
+    """What gdn_header_digest returns: include/libgdn.h without comments and blanks, digested."""
+    with open(os.path.join(ROOT, "include", "libgdn.h")) as f:
+        text = re.sub(r"/\*.*?\*/|//[^\n]*", " ", f.read(), flags=re.S)
+    return hashlib.sha256(" ".join(text.split()).encode()).hexdigest()[:16]
+
+
+def _digest_flag() -> str:
+    return '-DGDN_HEADER_DIGEST="%s"' % header_digest()
+
+
 def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC)
                   if f.endswith(".hip") or f.endswith(".cpp"))
@@ -66,7 +79,7 @@ def _compile(src: str) -> str:
     extra = FILE_FLAGS.get(os.path.basename(src), [])
     cmd = [hipcc()] + COMMON + DEVICE_FLAGS + extra + ["-c", src, "-o", obj]
     if src.endswith(".cpp"):
-        cmd = [hipcc()] + COMMON + ["-x", "hip"] + DEVICE_FLAGS + ["-c", src, "-o", obj]
+        cmd = [hipcc()] + COMMON + [_digest_flag(), "-x", "hip"] + DEVICE_FLAGS + ["-c", src, "-o", obj]
     res = subprocess.run(cmd, capture_output=True, text=True)
     noise = "is not a recognized feature for this target"
     err = "\n".join(l for l in res.stderr.splitlines() if noise not in l)
@@ -87,7 +100,7 @@ def _build_calls() -> str:
     # (pages_extend 15.5 -> 17.9 us on the host).
     tmp = CALLS + ".tmp%d" % os.getpid()
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-DNDEBUG", "-D__HIP_PLATFORM_AMD__=1",
-           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI]
+           _digest_flag(), "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI]
     for d in cpp_extension.include_paths() + [sysconfig.get_paths()["include"]]:
         cmd += ["-isystem", d]
     # torch's libraries are loaded before the module, so it carries no path to them

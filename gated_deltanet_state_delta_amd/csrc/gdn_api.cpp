@@ -72,6 +72,8 @@ const char* gdn_last_error(void) { return g_err; }
 
 const char* gdn_version(void) { return "0.1.0"; }
 
+const char* gdn_header_digest(void) { return GDN_HEADER_DIGEST; }  // (the build defines it)
+
 gdn_status gdn_gate(const float* A_log, const float* dt_bias, const void* a, const void* b,
                     int32_t ab_dtype, int64_t n_tokens, int32_t hv, float* log_decay_out,
                     float* gamma_out, float* beta_out, void* stream) {

@@ -76,6 +76,11 @@ const char* gdn_last_error(void);
 /* Library version as "major.minor.patch". */
 const char* gdn_version(void);
 
+/* Digest of this header, comments aside, as the library was built from it:
+ * argument structs grow between versions, and a program whose own build took
+ * another header must not call the library. */
+const char* gdn_header_digest(void);
+
 /* gdn_wait_timeouts -- health check of the in-kernel waits.
  *
  * The bf16 pair prefill kernel (and the scan's passes, which run it) hands
