@@ -90,7 +90,7 @@ def _compile(src: str) -> str:
     return obj
 
 
-def _build_calls() -> str:
+def _build_calls(tmp: str) -> None:
     import sysconfig
 
     import torch
@@ -98,7 +98,6 @@ def _build_calls() -> str:
     # NDEBUG: without it a header adds a thread-local variable to the module, and
     # with one loaded late every access to other libraries' ones goes a slow way
     # (pages_extend 15.5 -> 17.9 us on the host).
-    tmp = CALLS + ".tmp%d" % os.getpid()
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-DNDEBUG", "-D__HIP_PLATFORM_AMD__=1",
            _digest_flag(), "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI]
     for d in cpp_extension.include_paths() + [sysconfig.get_paths()["include"]]:
@@ -111,24 +110,33 @@ def _build_calls() -> str:
         raise RuntimeError("g++ failed for binding/calls.cpp:\n" + res.stderr)
     if res.stderr.strip():
         sys.stderr.write(res.stderr)
-    os.replace(tmp, CALLS)
-    return CALLS
+
+
+def _link(objs, tmp: str) -> None:
+    cmd = [hipcc(), "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp] + objs
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("link failed:\n" + res.stderr)
 
 
 def build(jobs: int | None = None) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
     jobs = jobs or min(len(srcs), max(1, min(16, os.cpu_count() or 1)))
-    with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
-        calls = ex.submit(_build_calls)
-        objs = list(ex.map(_compile, srcs))
-        calls.result()
-    tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [hipcc(), "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp] + objs
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError("link failed:\n" + res.stderr)
-    os.replace(tmp, LIB)
+    lib, calls = (path + ".tmp%d" % os.getpid() for path in (LIB, CALLS))
+    try:
+        with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+            module = ex.submit(_build_calls, calls)
+            objs = list(ex.map(_compile, srcs))
+            module.result()
+        _link(objs, lib)
+        # both together, and only when both are there: they belong to one header
+        os.replace(lib, LIB)
+        os.replace(calls, CALLS)
+    finally:
+        for tmp in (lib, calls):
+            if os.path.exists(tmp):
+                os.remove(tmp)
     return LIB
 
 

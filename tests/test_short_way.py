@@ -1,5 +1,6 @@
 """The short way's module (binding/calls.cpp) and the library that it is bound to, on the host."""
 import ctypes
+import subprocess
 
 import pytest
 
@@ -29,3 +30,39 @@ def test_a_library_of_another_header_is_refused(digest):
     module.bind(_address(lib.gdn_header_digest), *entries)
     with pytest.raises(TypeError):
         module.bind(*entries)
+
+
+@pytest.fixture
+def compilers(monkeypatch, tmp_path):
+    """A build into a folder of its own whose compilers only write their output's
+    name; those whose command holds a word of the list fail."""
+    fail = []
+
+    def run(cmd, **kw):
+        if any(word in arg for word in fail for arg in cmd):
+            return subprocess.CompletedProcess(cmd, 1, "", "refused")
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write("new")
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(B.subprocess, "run", run)
+    for name in ("LIB", "CALLS", "BUILD"):
+        monkeypatch.setattr(B, name, str(tmp_path / name))
+    return fail
+
+
+def _built(tmp_path):
+    return {p.name: p.read_text() for p in tmp_path.iterdir() if p.is_file()}
+
+
+@pytest.mark.parametrize("fails", ["gdn_pages.hip", "LIB.tmp", "calls.cpp"])
+def test_a_build_that_fails_leaves_the_pair_as_it_was(compilers, tmp_path, fails):
+    (tmp_path / "LIB").write_text("old")
+    (tmp_path / "CALLS").write_text("old")
+    compilers.append(fails)
+    with pytest.raises(RuntimeError):
+        B.build()
+    assert _built(tmp_path) == {"LIB": "old", "CALLS": "old"}
+    compilers.clear()
+    B.build()
+    assert _built(tmp_path) == {"LIB": "new", "CALLS": "new"}
