@@ -8,6 +8,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libgdn.so")
@@ -140,6 +141,7 @@ class PagesArgs(ctypes.Structure):
 _lock = threading.Lock()
 _lib = None
 _calls = None
+_no_calls = False  # whether loading the module has failed
 
 
 def load(path: str | None = None):
@@ -212,6 +214,21 @@ def calls():
                       ("header_digest", "attn_decode", "attn_decode_workspace_size", "kv_append", "kv_read", "rope")))
         _calls = module
     return _calls
+
+
+def short_way():
+    """calls(), or None where the module is missing or does not load: the calls then
+    go the general way in Python, with one warning."""
+    global _no_calls
+    if not _no_calls:
+        load()  # without the library there is no way at all
+        try:
+            return calls()
+        except (ImportError, RuntimeError) as e:
+            _no_calls = True
+            warnings.warn("calls of one token a row take 5 to 10 us longer on the host, without the module _calls: %s" % e,
+                          RuntimeWarning, stacklevel=4)
+    return None
 
 
 class GdnError(RuntimeError):

@@ -30,9 +30,12 @@ _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cud
 
 def _short(name, *args):
     """The call by the short way (binding/calls.cpp) on the current device and
-    stream, or None where it is not an ordinary one."""
+    stream, or None where it is not an ordinary one or the module is not there."""
+    module = _lib._calls or _lib.short_way()
+    if module is None:
+        return None
     dev = _current_device()
-    return getattr(_lib._calls or _lib.calls(), name)(*args, dev, _raw_stream(dev))
+    return getattr(module, name)(*args, dev, _raw_stream(dev))
 
 
 def _on(stream, dev, tensors):

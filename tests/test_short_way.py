@@ -1,10 +1,13 @@
 """The short way's module (binding/calls.cpp) and the library that it is bound to, on the host."""
 import ctypes
 import subprocess
+import sys
+import warnings
 
 import pytest
 
 import gated_deltanet_state_delta_amd._lib as L
+import gated_deltanet_state_delta_amd.paged as paged
 from gated_deltanet_state_delta_amd import build as B
 
 ENTRIES = ("attn_decode", "attn_decode_workspace_size", "kv_append", "kv_read", "rope")
@@ -66,3 +69,39 @@ def test_a_build_that_fails_leaves_the_pair_as_it_was(compilers, tmp_path, fails
     compilers.clear()
     B.build()
     assert _built(tmp_path) == {"LIB": "new", "CALLS": "new"}
+
+
+@pytest.fixture
+def unbound(monkeypatch):
+    """As in a process that has not used the short way yet."""
+    monkeypatch.setattr(L, "_calls", None)
+    monkeypatch.setattr(L, "_no_calls", False)
+    monkeypatch.delitem(sys.modules, L.__package__ + "._calls", raising=False)
+
+
+@pytest.mark.parametrize("why", ["missing", "other torch", "other header"])
+def test_without_the_module_calls_go_the_general_way(unbound, monkeypatch, tmp_path, why):
+    lib = L.load()
+    if why == "missing":
+        monkeypatch.setattr(L, "PKG", str(tmp_path))
+    elif why == "other torch":
+        monkeypatch.setitem(sys.modules, L.__package__ + "._calls", None)  # importing it raises ImportError
+        monkeypatch.delattr(sys.modules[L.__package__], "_calls", raising=False)
+    else:
+        class Other:
+            gdn_header_digest = lib.gdn_version
+            __getattr__ = lambda self, name: getattr(lib, name)
+        monkeypatch.setattr(L, "_lib", Other())
+    with pytest.warns(RuntimeWarning, match="_calls"):
+        assert paged._short("rope", None) is None
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")  # one warning only
+        assert paged._short("kv_append", None) is None
+
+
+def test_without_the_library_there_is_no_way(unbound, monkeypatch, tmp_path):
+    monkeypatch.setattr(L, "_lib", None)
+    monkeypatch.setattr(L, "LIB_PATH", str(tmp_path / "libgdn.so"))
+    with pytest.raises(Exception):
+        paged._short("rope", None)
+    assert not L._no_calls
