@@ -58,7 +58,7 @@ def _built(tmp_path):
     return {p.name: p.read_text() for p in tmp_path.iterdir() if p.is_file()}
 
 
-@pytest.mark.parametrize("fails", ["gdn_pages.hip", "LIB.tmp", "calls.cpp"])
+@pytest.mark.parametrize("fails", ["gdn_pages.hip", "LIB.tmp"])
 def test_a_build_that_fails_leaves_the_pair_as_it_was(compilers, tmp_path, fails):
     (tmp_path / "LIB").write_text("old")
     (tmp_path / "CALLS").write_text("old")
@@ -69,6 +69,26 @@ def test_a_build_that_fails_leaves_the_pair_as_it_was(compilers, tmp_path, fails
     compilers.clear()
     B.build()
     assert _built(tmp_path) == {"LIB": "new", "CALLS": "new"}
+
+
+@pytest.mark.parametrize("why", ["no compiler", "no headers", "no torch"])
+def test_the_library_is_built_without_the_module(compilers, monkeypatch, tmp_path, capsys, why):
+    """An old module beside it would be one of another header: it goes."""
+    (tmp_path / "CALLS").write_text("old")
+    if why == "no headers":
+        compilers.append("calls.cpp")
+    elif why == "no torch":
+        monkeypatch.setitem(sys.modules, "torch", None)
+    else:
+        run = B.subprocess.run
+
+        def none(cmd, **kw):
+            if any("calls.cpp" in arg for arg in cmd):
+                raise FileNotFoundError("g++")
+            return run(cmd, **kw)
+        monkeypatch.setattr(B.subprocess, "run", none)
+    B.build()
+    assert _built(tmp_path) == {"LIB": "new"} and "general way" in capsys.readouterr().err
 
 
 @pytest.fixture
