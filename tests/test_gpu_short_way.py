@@ -1,4 +1,7 @@
 """The short way into libgdn (binding/calls.cpp) on the GPU: what a program keeps without it."""
+import ctypes
+import threading
+
 import pytest
 import torch
 
@@ -42,3 +45,52 @@ def test_every_call_works_without_the_module(monkeypatch):
     monkeypatch.setattr(L, "_no_calls", True)
     assert _short("rope", q, k, f, args[3], None, None, False, 1.0) is None
     assert all(torch.equal(a, b) for a, b in zip(want, run()))
+
+
+def _entries(lib):
+    return [ctypes.cast(getattr(lib, "gdn_" + n), ctypes.c_void_p).value
+            for n in ("header_digest", "attn_decode", "attn_decode_workspace_size", "kv_append", "kv_read", "rope")]
+
+
+def test_other_threads_run_while_libgdn_does():
+    """With the interpreter's own check of its lock in the place of libgdn's entries (nothing is launched): 0, as
+    GDN_OK, where the calling thread does not hold it."""
+    args, scales = _state()
+    q, k = torch.randn(4, 1, 6, 64).bfloat16().cuda(), torch.randn(4, 1, 2, 64).bfloat16().cuda()
+    f = gdn.rope_frequencies(64)[0].cuda()
+    ks, vs = scales.values()
+    module, entries = L.calls(), _entries(L.load())
+    check = ctypes.cast(ctypes.pythonapi.PyGILState_Check, ctypes.c_void_p).value
+    try:
+        module.bind(entries[0], *[check] * 5)
+        got = [_short("attn_decode", q, *args, None, ks, vs), _short("kv_append", k, k, *args, None, ks, vs),
+               _short("kv_read", *args, 3, None, 1, ks, vs), _short("rope", q, k, f, args[3], None, None, False, 1.0)]
+    finally:
+        module.bind(*entries)
+    assert all(x is not None for x in got)
+
+
+def test_calls_of_several_threads():
+    args, scales = _state((3000, 40, 700, 1))
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q = [torch.randn(4, 1, 6, 64, generator=g, device="cuda").bfloat16() for _ in range(4)]
+    f = gdn.rope_frequencies(64)[0].cuda()
+    call = lambda x: [gdn.attn_decode(x, *args, **scales), *gdn.kv_read(*args, 30, **scales), gdn.rope(x, None, f, lens=args[3])[0]]
+    want = [call(x) for x in q]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(50):
+                got = call(q[i])
+                torch.cuda.current_stream().synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                    wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
