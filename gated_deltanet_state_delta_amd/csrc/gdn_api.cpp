@@ -315,10 +315,23 @@ static gdn_status cache_sizes(const char* f, int32_t batch, int32_t hkv, int32_t
   return GDN_OK;
 }
 
+// The tokens of a block of block scales, 0 without them.
+static gdn_status block_size(const char* f, int32_t cache_dtype, int32_t page_size, int32_t block) {
+  if (block < 0) return fail(GDN_ERR_SHAPE, "%s: scale_block=%d", f, block);
+  if (block == 0) return GDN_OK;
+  if (cache_dtype != GDN_E4M3 && cache_dtype != GDN_I8)
+    return fail(GDN_ERR_SHAPE, "%s: block scales are for 8-bit caches", f);
+  if (block > page_size || page_size % block != 0)
+    return fail(GDN_ERR_SHAPE, "%s: scale_block=%d does not divide page_size=%d", f, block, page_size);
+  if (block > 65536) return fail(GDN_ERR_UNSUPPORTED, "%s: scale_block=%d (supported up to 65536)", f, block);
+  return GDN_OK;
+}
+
 // The scales of a cache: a factor a head, or block scales.
 static gdn_status scales_check(const char* f, int32_t cache_dtype, int32_t n_pages, int32_t page_size, const float* k_scale,
                                const float* v_scale, int32_t block, const float* k_blocks, const float* v_blocks) {
-  if (block < 0) return fail(GDN_ERR_SHAPE, "%s: scale_block=%d", f, block);
+  const gdn_status st = block_size(f, cache_dtype, page_size, block);
+  if (st != GDN_OK) return st;
   if (block == 0) {
     if (k_blocks || v_blocks) return fail(GDN_ERR_SHAPE, "%s: block scales need scale_block", f);
     if (cache_dtype == GDN_I8) return fail(GDN_ERR_NULL, "%s: an int8 cache needs block scales", f);
@@ -328,12 +341,7 @@ static gdn_status scales_check(const char* f, int32_t cache_dtype, int32_t n_pag
       return fail(GDN_ERR_SHAPE, "%s: k_scale and v_scale are for e4m3 caches", f);
     return GDN_OK;
   }
-  if (cache_dtype != GDN_E4M3 && cache_dtype != GDN_I8)
-    return fail(GDN_ERR_SHAPE, "%s: block scales are for 8-bit caches", f);
   if (k_scale || v_scale) return fail(GDN_ERR_SHAPE, "%s: k_scale and v_scale with block scales", f);
-  if (block > page_size || page_size % block != 0)
-    return fail(GDN_ERR_SHAPE, "%s: scale_block=%d does not divide page_size=%d", f, block, page_size);
-  if (block > 65536) return fail(GDN_ERR_UNSUPPORTED, "%s: scale_block=%d (supported up to 65536)", f, block);
   if (n_pages > 0 && (!k_blocks || !v_blocks)) return fail(GDN_ERR_NULL, "%s: k_block_scale and v_block_scale are required", f);
   if (!aligned(k_blocks, 4) || !aligned(v_blocks, 4))
     return fail(GDN_ERR_LAYOUT, "%s: block scales must be 4-byte aligned", f);
@@ -394,7 +402,7 @@ size_t gdn_attn_decode_workspace_size(const gdn_attn_decode_args* args) {
   const gdn_attn_decode_args& a = *args;
   // the split's arithmetic holds for sizes that the call takes
   if (cache_sizes(f, a.batch, a.hkv, a.d, a.io_dtype, a.cache_dtype, a.n_pages, a.page_size, a.max_pages) != GDN_OK ||
-      attn_sizes(f, a) != GDN_OK)
+      block_size(f, a.cache_dtype, a.page_size, a.scale_block) != GDN_OK || attn_sizes(f, a) != GDN_OK)
     return 0;
   return gdn::attn_workspace_bytes(a);
 }

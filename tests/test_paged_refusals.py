@@ -1,0 +1,22 @@
+"""More refusals of the paged-cache calls and of rope on the host (no GPU needed)."""
+import ctypes
+
+import pytest
+
+import gated_deltanet_state_delta_amd._lib as L
+from test_block_scales_abi import BLOCKS
+from test_paged_abi import _attn
+
+LONG = dict(batch=1, max_pages=1000, page_table_stride=1000)
+
+
+@pytest.mark.parametrize("over", [
+    dict(scale_block=-8), dict(scale_block=5), dict(scale_block=32), dict(cache_dtype=1), dict(cache_dtype=1, scale_block=-1),
+    dict(page_size=1 << 17, scale_block=1 << 17),
+])
+def test_the_workspace_of_a_scale_block_that_the_call_refuses_is_0(over):
+    lib = L.load()
+    assert lib.gdn_attn_decode_workspace_size(ctypes.byref(_attn(**{**LONG, **BLOCKS}))) > 0
+    a = _attn(**{**LONG, **BLOCKS, **over})
+    assert lib.gdn_attn_decode(ctypes.byref(a), None) in (2, 5)
+    assert lib.gdn_attn_decode_workspace_size(ctypes.byref(a)) == 0
