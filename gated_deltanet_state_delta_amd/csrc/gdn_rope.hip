@@ -29,7 +29,7 @@ struct RopeParams {
   int64_t total;
   float factor;
   int batch, T, hq, hkv, d, rot, run, pos_i64, zero_rest;
-  int q_copy, k_copy;  // whether the dimensions behind rot are copied (not in place)
+  int q_copy, k_copy;  // whether the dimensions behind rot are written: not in place, unless tokens of no row get zeros
 };
 
 constexpr int kRopeRun = 64;      // most tokens of one workgroup
@@ -218,8 +218,8 @@ hipError_t launch_rope(const gdn_rope_args& a, hipStream_t stream) {
   p.hkv = a.k ? a.hkv : 0;
   p.d = a.d;
   p.rot = a.rot;
-  p.q_copy = a.q != a.q_out;
-  p.k_copy = a.k != a.k_out;
+  p.q_copy = a.q != a.q_out || a.zero_rest;
+  p.k_copy = a.k != a.k_out || a.zero_rest;
   const bool interleaved = a.interleaved != 0;
   int v = a.io_dtype == GDN_BF16 ? 8 : 4;
   while (((interleaved ? a.rot : a.rot / 2) | (a.d - a.rot)) % v != 0) v /= 2;
