@@ -506,6 +506,13 @@ gdn_status gdn_kv_read(const gdn_kv_read_args* p, void* stream) {
   return from_hip(gdn::launch_kv_read(a, (hipStream_t)stream), "gdn_kv_read launch");
 }
 
+// Whether rows of d elements, of so many tokens and heads, keep apart: one of the two strides holds all of the other's.
+static bool rows_apart(int64_t tokens, int64_t token, int64_t heads, int64_t head, int64_t d) {
+  const bool heads_inside = (heads == 1 || head >= d) && (tokens == 1 || token >= (heads - 1) * head + d);
+  const bool tokens_inside = (tokens == 1 || token >= d) && (heads == 1 || head >= (tokens - 1) * token + d);
+  return heads_inside || tokens_inside;
+}
+
 // One input and output of gdn_rope.
 static gdn_status rope_layout(const char* f, const char* name, const gdn_rope_args& a, int32_t heads, const void* in,
                               int64_t st, int64_t sh, const void* out, int64_t ot, int64_t oh) {
@@ -514,6 +521,7 @@ static gdn_status rope_layout(const char* f, const char* name, const gdn_rope_ar
   const int64_t lim = int64_t(1) << 40;
   if (st < 0 || sh < 0 || ot < 0 || oh < 0 || st >= lim || sh >= lim || ot >= lim || oh >= lim)
     return fail(GDN_ERR_LAYOUT, "%s: strides of %s must be in [0, 2^40)", f, name);
+  if (!rows_apart(a.total_tokens, ot, heads, oh, a.d)) return fail(GDN_ERR_LAYOUT, "%s: rows of the output of %s overlap", f, name);
   if (in == out) {
     if ((a.total_tokens > 1 && st != ot) || (heads > 1 && sh != oh))
       return fail(GDN_ERR_LAYOUT, "%s: %s in place needs equal strides", f, name);

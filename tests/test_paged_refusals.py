@@ -4,8 +4,8 @@ import ctypes
 import pytest
 
 import gated_deltanet_state_delta_amd._lib as L
-from test_block_scales_abi import BLOCKS
-from test_paged_abi import _attn
+from test_block_scales_abi import BLOCKS, _rope
+from test_paged_abi import FAKE, _attn
 
 LONG = dict(batch=1, max_pages=1000, page_table_stride=1000)
 
@@ -20,3 +20,16 @@ def test_the_workspace_of_a_scale_block_that_the_call_refuses_is_0(over):
     a = _attn(**{**LONG, **BLOCKS, **over})
     assert lib.gdn_attn_decode(ctypes.byref(a), None) in (2, 5)
     assert lib.gdn_attn_decode_workspace_size(ctypes.byref(a)) == 0
+
+
+@pytest.mark.parametrize("over", [
+    dict(qo_stride_token=64), dict(qo_stride_token=383), dict(qo_stride_token=0), dict(qo_stride_head=0), dict(qo_stride_head=63),
+    dict(ko_stride_token=0), dict(ko_stride_head=32, ko_stride_token=96), dict(ko_stride_head=511, ko_stride_token=64),
+    dict(total_tokens=1, batch=1, qo_stride_head=8),
+    dict(q_out=FAKE, q_stride_token=0, qo_stride_token=0), dict(k_out=FAKE * 2, k_stride_head=0, ko_stride_head=0),  # in place
+])
+def test_rope_refuses_outputs_whose_rows_overlap(over):
+    """Threads would write one place with different values."""
+    lib = L.load()
+    assert lib.gdn_rope(ctypes.byref(_rope(**over)), None) == 4, lib.gdn_last_error()
+    assert b"overlap" in lib.gdn_last_error()
