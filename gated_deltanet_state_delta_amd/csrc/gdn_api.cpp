@@ -491,6 +491,14 @@ gdn_status gdn_kv_append(const gdn_kv_append_args* p, void* stream) {
   return from_hip(gdn::launch_kv_quantise(a, (hipStream_t)stream), "gdn_kv_append launch");
 }
 
+// Whether rows of d elements, of so many tokens and heads, keep apart: one of the two strides holds all of the other's.
+static bool rows_apart(int64_t tokens, int64_t token, int64_t heads, int64_t head, int64_t d) {
+  typedef __int128 wide;  // strides are any int64
+  const bool heads_inside = (heads == 1 || head >= d) && (tokens == 1 || token >= (wide)(heads - 1) * head + d);
+  const bool tokens_inside = (tokens == 1 || token >= d) && (heads == 1 || head >= (wide)(tokens - 1) * token + d);
+  return heads_inside || tokens_inside;
+}
+
 gdn_status gdn_kv_read(const gdn_kv_read_args* p, void* stream) {
   static const char* f = "gdn_kv_read";
   g_err[0] = 0;
@@ -503,14 +511,10 @@ gdn_status gdn_kv_read(const gdn_kv_read_args* p, void* stream) {
     return fail(GDN_ERR_NULL, "%s: k, v, caches, page_table and lens are required", f);
   st = tokens_layout(f, a);
   if (st != GDN_OK) return st;
+  if (!rows_apart(a.total_tokens, a.k_stride_token, a.hkv, a.k_stride_head, a.d) ||
+      !rows_apart(a.total_tokens, a.v_stride_token, a.hkv, a.v_stride_head, a.d))
+    return fail(GDN_ERR_LAYOUT, "%s: rows of k or v overlap", f);
   return from_hip(gdn::launch_kv_read(a, (hipStream_t)stream), "gdn_kv_read launch");
-}
-
-// Whether rows of d elements, of so many tokens and heads, keep apart: one of the two strides holds all of the other's.
-static bool rows_apart(int64_t tokens, int64_t token, int64_t heads, int64_t head, int64_t d) {
-  const bool heads_inside = (heads == 1 || head >= d) && (tokens == 1 || token >= (heads - 1) * head + d);
-  const bool tokens_inside = (tokens == 1 || token >= d) && (heads == 1 || head >= (tokens - 1) * token + d);
-  return heads_inside || tokens_inside;
 }
 
 // One input and output of gdn_rope.

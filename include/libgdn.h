@@ -585,7 +585,8 @@ gdn_status gdn_kv_append(const gdn_kv_append_args* args, void* stream);
  * its scale for 8-bit caches), rounded once to io_dtype.  Tokens at positions
  * that hold nothing (negative, past the table, an invalid page entry) get zeros.
  *
- *   k, v  [total_tokens, hkv, d] io_dtype, strides {token, head}; written
+ *   k, v  [total_tokens, hkv, d] io_dtype, strides {token, head}; written;
+ *         rows that overlap are GDN_ERR_LAYOUT
  *   cu_seqlens  as for gdn_kv_append; tokens of no row are left as they were,
  *         or get zeros with zero_rest != 0
  * k and v must not overlap each other or the caches (not checked).  cache_dtype

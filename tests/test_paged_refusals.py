@@ -4,7 +4,7 @@ import ctypes
 import pytest
 
 import gated_deltanet_state_delta_amd._lib as L
-from test_block_scales_abi import BLOCKS, _rope
+from test_block_scales_abi import BLOCKS, _read, _rope
 from test_paged_abi import FAKE, _attn
 
 LONG = dict(batch=1, max_pages=1000, page_table_stride=1000)
@@ -32,4 +32,14 @@ def test_rope_refuses_outputs_whose_rows_overlap(over):
     """Threads would write one place with different values."""
     lib = L.load()
     assert lib.gdn_rope(ctypes.byref(_rope(**over)), None) == 4, lib.gdn_last_error()
+    assert b"overlap" in lib.gdn_last_error()
+
+
+@pytest.mark.parametrize("over", [
+    dict(k_stride_token=0), dict(v_stride_token=0), dict(k_stride_head=0), dict(v_stride_head=32), dict(k_stride_token=64),
+    dict(v_stride_token=64, v_stride_head=192), dict(total_tokens=1, batch=1, v_stride_head=56),
+])
+def test_kv_read_refuses_outputs_whose_rows_overlap(over):
+    lib = L.load()
+    assert lib.gdn_kv_read(ctypes.byref(_read(**over)), None) == 4, lib.gdn_last_error()
     assert b"overlap" in lib.gdn_last_error()
