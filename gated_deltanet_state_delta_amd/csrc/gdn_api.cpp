@@ -533,8 +533,15 @@ static gdn_status rope_layout(const char* f, const char* name, const gdn_rope_ar
   }
   auto span = [&](int64_t t, int64_t h) { return ((size_t)(a.total_tokens - 1) * t + (size_t)(heads - 1) * h + a.d) * es; };
   const uintptr_t i0 = (uintptr_t)in, o0 = (uintptr_t)out;
-  if (i0 < o0 + span(ot, oh) && o0 < i0 + span(st, sh)) return fail(GDN_ERR_LAYOUT, "%s: the output of %s overlaps it", f, name);
-  return GDN_OK;
+  if (i0 >= o0 + span(ot, oh) || o0 >= i0 + span(st, sh)) return GDN_OK;
+  // slices of one buffer: tokens the same stride apart, the output's heads in the gaps between the input's
+  const int64_t gap = ot * (int64_t)es;
+  if (st == ot && gap > 0) {
+    const int64_t in_heads = ((heads - 1) * sh + a.d) * (int64_t)es, out_heads = ((heads - 1) * oh + a.d) * (int64_t)es;
+    const int64_t behind = ((int64_t)(o0 - i0) % gap + gap) % gap;  // from an input's token to the next output's
+    if (behind >= in_heads && behind + out_heads <= gap) return GDN_OK;
+  }
+  return fail(GDN_ERR_LAYOUT, "%s: the output of %s overlaps it", f, name);
 }
 
 gdn_status gdn_rope(const gdn_rope_args* p, void* stream) {

@@ -152,8 +152,8 @@ def rope(q, k, inv_freq, *, lens=None, cu_seqlens=None, positions=None, interlea
     A token's position follows from lens [B] as in kv_append: lens[b] - n + i for
     token i of row b's n, T for every row or with cu_seqlens [B + 1] packed; or
     positions, of q's leading shape, gives it.  Angles are formed in 64 bits.
-    out: (q, k) to write to, which may be the inputs (each its own, or slices of
-    one buffer that do not overlap); new tensors when None.
+    out: (q, k) to write to: each its own input, or apart from both, also as
+    slices of one buffer that do not overlap; new tensors when None.
     Packed tokens of no row are left as they were there, and zeros in new ones.
     Returns (q, k).
     """

@@ -642,8 +642,10 @@ gdn_status gdn_kv_read(const gdn_kv_read_args* args, void* stream);
  *             gdn_kv_append (read where positions is NULL); tokens of no row
  *             are left as they were in the outputs, or get zeros with
  *             zero_rest != 0
- * An output may be its input (equal pointer and strides); other overlaps, rows
- * of an output over each other among them, are GDN_ERR_LAYOUT.  rot is even,
+ * An output may be its input (equal pointer and strides), or a slice of the same
+ * buffer (one token stride, its heads between those of the input's tokens); other
+ * overlaps, rows of an output over each other among them, are GDN_ERR_LAYOUT, and
+ * so are rows dealt out in turn in other ways.  rot is even,
  * 2 <= rot <= d <= 1024; hq + hkv at most 65536; total_tokens at most 2^24;
  * pointers aligned to their element.  q_out starts neither at k nor at k_out,
  * and k_out not at q (GDN_ERR_LAYOUT); rows of q_out must not overlap those of

@@ -35,6 +35,13 @@ def test_rope_refuses_outputs_whose_rows_overlap(over):
     assert b"overlap" in lib.gdn_last_error()
 
 
+@pytest.mark.parametrize("at,stride", [(300, 768), (383, 768), (385, 768), (400, 700), (768 + 300, 768), (-300, 768), (384, 767)])
+def test_rope_refuses_slices_that_overlap(at, stride):
+    """Queries of 6 heads of 64 in rows of `stride`, their output `at` elements behind them."""
+    a = _rope(q_stride_token=stride, qo_stride_token=stride, q_out=FAKE + 2 * at)
+    assert L.load().gdn_rope(ctypes.byref(a), None) == 4 and b"overlap" in L.load().gdn_last_error()
+
+
 @pytest.mark.parametrize("over", [
     dict(k_stride_token=0), dict(v_stride_token=0), dict(k_stride_head=0), dict(v_stride_head=32), dict(k_stride_token=64),
     dict(v_stride_token=64, v_stride_head=192), dict(total_tokens=1, batch=1, v_stride_head=56),
