@@ -13,8 +13,9 @@ namespace gdn {
 // join with sixteen and with four: 12 rows of hundreds of parts (3 rows of
 // 19 620 tokens, fp32) 32.8 and 34.8 us, 18 rows (19 870 tokens, heads of 256)
 // 42.0 and 45.8, 156 rows of few parts the same.  Four also for up to 32 parts a
-// row of a block-scaled cache, which they load at once (1 row of 1003 tokens, 8
-// heads of 128: 9.6 us against 10.1; 4 rows 10.6 and 11.2; 2 rows of 1500 the same).
+// row, taken over the batch, of a block-scaled cache, which they load at once (1 row
+// of 1003 tokens, 8 heads of 128: 9.6 us against 10.1; 4 rows 10.6 and 11.2; 2 rows
+// of 1500 the same).  Other caches keep the choice that was measured for them.
 template <typename IO, int D, int WPR>
 __global__ void __launch_bounds__(WPR > 1 ? 64 * WPR : 256) attn_join_kernel(AttnParams p) {
   constexpr int V = D < 64 ? 1 : D / 64;  // dimensions of a lane (the first 32 lanes' for D = 32)
@@ -139,7 +140,8 @@ static int attn_shares(const gdn_attn_decode_args& a) {
 // while two such workgroups a CU hold everything at a time or two (8 heads of 128,
 // bf16 over e4m3: 1 row of 256 tokens 7.3 us against 10.3, of 512 9.6 against
 // 11.0, of 1024 16 against 11; 64 rows of 256 12.6 against 17, of 512 19 against
-// 23; 256 rows of 256 35 against 30).
+// 23; 256 rows of 256 35 against 30).  Teams of eight waves were slower.  Other
+// caches keep one wave, up to the 128 tokens that attn_shares measured for them.
 static bool attn_team(const gdn_attn_decode_args& a) {
   const int64_t cap = (int64_t)a.max_pages * a.page_size;
   return a.scale_block > 0 && cap > 64 && cap <= 512 && (int64_t)a.batch * a.hkv * attn_tiles(a) <= 1024;

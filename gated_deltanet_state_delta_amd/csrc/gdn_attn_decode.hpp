@@ -45,7 +45,8 @@
 namespace gdn {
 
 // Block scales: a key's factor enters its score, a value's the weight before
-// the product.  A lane holds four neighbouring keys' scores.
+// the product (bf16 queries: the two bf16 terms hold weight times factor to
+// 2^-16).  A lane holds four neighbouring keys' scores.
 //  * kBlocksWide: blocks of 4, 8 or a multiple of 16 tokens, pages of a multiple
 //    of 16: one factor for the four, loaded where it is (the subtile's first
 //    factor through a scalar, the lane's own at a fixed offset from there);
@@ -58,7 +59,8 @@ namespace gdn {
 // e4m3, a block a page, 537 MB: 89 us = 6.0 TB/s, 98 without these; 64 ragged rows
 // up to 8192 tokens, 8 heads of 128, int8, blocks of one token, 572 MB: 105 us = 5.4
 // TB/s, where the factors of every key are loaded and multiplied in besides.  Rows
-// of 64 bytes stay at 4.5 TB/s, of 32 at 2.8.
+// of 64 bytes stay at 4.2 to 4.5 TB/s, of 32 at 2.7: their pieces of V are 4 and 2
+// bytes a lane (VW), so a tile takes 8 and 16 loads of values.
 // Whether it is one of the first two.
 static inline bool attn_lane_blocks(int page_size, int block) {
   return page_size % 16 == 0 && (block == 1 || block == 4 || block == 8 || block % 16 == 0);
@@ -257,15 +259,16 @@ __device__ __forceinline__ float sum_over_g(float v) {
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// How many waves a SIMD holds and the bytes of K in a wave's tile.  Either
-// way 64 KiB a CU are in flight; fewer and longer streams read HBM faster as
+// How many waves a SIMD holds and the bytes of K in a wave's tile.  Without
+// block scales 64 KiB a CU are in flight either way; fewer and longer streams read HBM faster as
 // long as a wave's own work between its loads is short.  bf16 and fp32 rows of
 // 256 bytes and more: one wave, 8 KiB (64 ragged rows up to 8192 tokens, 8
 // heads of 128, bf16: 172 us; two waves of 4 KiB 175, two of 8 KiB 184, three
 // 193).  Shorter rows, and e4m3 whose conversion is VALU work: two waves, 4
 // KiB (256 rows, 2 heads of 256, e4m3: 110 us; one wave 131, three 122).
 // With block scales heads of 64 and fewer take 2 KiB (64 ragged rows up to 8192
-// tokens, 16 heads of 64, int8: 140 us, 4 KiB 159; heads of 128 gain 2% or lose 5%).
+// tokens, 16 heads of 64, int8: 140 us, 4 KiB 159; heads of 128 gain 2% or lose 5%),
+// and so half as many bytes are in flight, as with one wave (see attn_shares).
 constexpr int attn_occ(int es, int d) { return es > 1 && d >= 128 ? 1 : 2; }
 
 // IO: type of q and out; KE: cache element.  The products are bf16, or fp32
@@ -322,7 +325,7 @@ __global__ void __launch_bounds__(256, (AttnCfg<IO, KE, D, KIND, BS != kBlocksNo
   // up to 8192 tokens, 16 heads of 64, e4m3: 126 us against 136; of 32: 101 against
   // 129).  In caches of heads first there is no such neighbour and this costs 11%
   // (108 us against 97); a branch on the strides here costs every layout its
-  // overlapped loads (133 us).
+  // overlapped loads (133 us), an instantiation for each is not built.
   constexpr bool BF = C::BF, MT = KIND > 0;
   constexpr bool ONCE = (KIND < 2 || (KIND == 2 && RT == 2)) && (BS == kBlocksNone || D * ES >= 128);
   constexpr uint64_t kNone = ~0ull;

@@ -6,7 +6,8 @@
 // workgroup takes a run of tokens: their rot / 2 sines and cosines, which all
 // heads share, are formed once in LDS, then every thread turns pieces.  The
 // angle is formed in fp64 and reduced to turns there (fp32 would be 0.06 rad off
-// at position 10^6), sine and cosine in fp32.
+// at position 10^6), sine and cosine in fp32: fp32 results are 5.4e-8 off on
+// average, 4.0e-8 with sine and cosine in fp64; bf16 rounds 10^4 times as far.
 //
 // Measured: 32768 tokens of 32 + 8 heads of 128, bf16, 671 MB: 128 us = 5.2 TB/s,
 // over a large copy's 4.9; 8192 of 16 + 4 heads of 96, two thirds of each turned,
@@ -221,6 +222,8 @@ hipError_t launch_rope(const gdn_rope_args& a, hipStream_t stream) {
   p.q_copy = a.q != a.q_out || a.zero_rest;
   p.k_copy = a.k != a.k_out || a.zero_rest;
   const bool interleaved = a.interleaved != 0;
+  // One piece size for all of a head: 16384 tokens of 40 heads, bf16, heads of 128 turned whole 59 us, to rot 126 in
+  // pieces of 2 bytes 148 (neighbouring pairs, of 4 bytes, 138); heads of 80 whole 48, to rot 20 102 and 59.
   int v = a.io_dtype == GDN_BF16 ? 8 : 4;
   while (((interleaved ? a.rot : a.rot / 2) | (a.d - a.rot)) % v != 0) v /= 2;
   // Tokens per workgroup: about two rounds of what its threads hold (32768 tokens of 40
